@@ -129,7 +129,10 @@ __device__ __forceinline__ uint32_t ring_parity(int item, int depth) {
 // [0, dp_tiles) run whole, round robin (CTA c takes c, c + G, ...; G =
 // gridDim.x); the U = (tiles - dp_tiles) x KB slabs of the other tiles, in
 // tile-major order, run stream-K: CTA c takes the contiguous range
-// [c U / G, (c + 1) U / G), so every CTA gets the same share within one slab.
+// [c U / S, (c + 1) U / S) with S = min(G, U), so every CTA gets the same share
+// within one slab, and with fewer slabs than CTAs the first U take one each
+// (a CTA in the middle of a split tile must not be without a slab: the
+// fix-up reads a partial from every CTA between the tile's first and last).
 // A stream-K tile may be split across consecutive CTAs; only a CTA's first
 // and last stream-K segments can be partial. dp_tiles = 0 is pure stream-K,
 // dp_tiles = tiles pure round robin.
@@ -140,8 +143,10 @@ struct Schedule {
   __device__ Schedule(int kb_per_tile, int tiles, int dp)
       : tile(static_cast<int>(blockIdx.x)), KB(kb_per_tile), dp_tiles(dp) {
     const int64_t U = static_cast<int64_t>(tiles - dp) * kb_per_tile;
-    first = u = static_cast<int>(U * blockIdx.x / gridDim.x);
-    end = static_cast<int>(U * (blockIdx.x + 1) / gridDim.x);
+    const int64_t S = U < gridDim.x ? U : gridDim.x;
+    const bool some = blockIdx.x < S;
+    first = u = some ? static_cast<int>(U * blockIdx.x / S) : 0;
+    end = some ? static_cast<int>(U * (blockIdx.x + 1) / S) : 0;
   }
   __device__ int slabs() const {
     const int dp = tile < dp_tiles ? ((dp_tiles - 1 - tile) / static_cast<int>(gridDim.x) + 1) * KB : 0;
@@ -616,7 +621,8 @@ __global__ void __launch_bounds__(512, 1)
 constexpr int kStreamKMaxCtas = 160;
 
 // The tiles a stream-K launch splits across CTAs, worked out on the host:
-// CTA c holds slabs [c U / G, (c + 1) U / G) of the U = tiles x KB slabs, so
+// CTA c holds slabs [c U / G, (c + 1) U / G) of the U = tiles x KB slabs (G the
+// CTAs that have any: at most U), so
 // a tile is split when a range boundary falls inside it. Each split tile
 // lists its first contributor c0 (whose last segment it is), the number of
 // contributors, and the workspace slot c0 wrote (0 if the tile was also
@@ -777,7 +783,8 @@ cudaError_t launch_bt(const Launch& L, const uint16_t* x, int64_t ldx, const uin
     if (e != cudaSuccess) return e;
   }
   if (dp_tiles == tiles || grid < 2) return cudaSuccess;
-  SplitTiles st = split_tiles(tiles - dp_tiles, KB, grid);
+  const int64_t U = (tiles - dp_tiles) * KB;
+  SplitTiles st = split_tiles(tiles - dp_tiles, KB, U < grid ? U : grid);
   if (st.count == 0) return cudaSuccess;
   for (int i = 0; i < st.count; ++i) st.tile[i] += static_cast<int>(dp_tiles);
   const int mt = static_cast<int>(M < TOK ? M : TOK);
