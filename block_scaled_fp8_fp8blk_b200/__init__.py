@@ -19,6 +19,10 @@ __all__ = [
     "linear_w8a8", "linear_w8a8_quantized", "workspace_size", "encode_e4m3", "read_device_error",
     "version", "LinearJob", "stream_slot_bytes", "streamed_linears", "selftest_wait_timeout",
     "LinearArgs", "linear_sequence",
+    "ACTIVATIONS", "Epilogue", "linear_w8a16_epilogue", "linear_w8a8_epilogue",
+    "gated_linear_w8a16", "gated_linear_w8a8", "gated_backward", "epilogue_backward",
+    "epilogue_backward_workspace_size", "transpose_weight", "transpose_gated_weights",
+    "linear_grad_weight",
     "LIB_PATH", "EXPORTS",
 ]
 
@@ -48,6 +52,21 @@ class LinearArgs(ctypes.Structure):
                 ("scale_inv", _p), ("y", _p), ("ldy", _i64), ("M", _i64), ("N", _i64), ("K", _i64)]
 
 
+class Epilogue(ctypes.Structure):
+    """fp8blk_epilogue: what follows a linear's product."""
+    _fields_ = [("bias", _p), ("activation", ctypes.c_int32), ("residual", _p), ("ldr", _i64),
+                ("preact", _p), ("ldp", _i64)]
+
+
+# fp8blk_activation by name
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+_i32 = ctypes.c_int32
+_linear_epilogue_args = [_p, _i64, _p, _i64, _p, _p, _i64, _i64, _i64, _i64,
+                         ctypes.POINTER(Epilogue), _p, _sz, _p]
+_gated_linear_args = [_p, _i64, _p, _p, _p, _p, _i64, _i32, _p, _i64, _p, _p, _i64, _i64, _i64, _i64,
+                      _p, _sz, _p]
+
 # name -> (restype, argtypes), mirroring include/fp8blk.h
 EXPORTS = {
     "fp8blk_quantize_weight": (_st, [_p, _i64, _i64, _i64, _p, _i64, _p, _p]),
@@ -62,6 +81,15 @@ EXPORTS = {
     "fp8blk_linear_sequence": (_st, [ctypes.POINTER(LinearArgs), _i64, _p, _sz, _p]),
     "fp8blk_streamed_linears": (_st, [ctypes.POINTER(LinearJob), _i64, _p, _sz, ctypes.c_int32,
                                       _p, _sz, _p, _p, ctypes.POINTER(_p)]),
+    "fp8blk_linear_w8a16_epilogue": (_st, _linear_epilogue_args),
+    "fp8blk_linear_w8a8_epilogue": (_st, _linear_epilogue_args),
+    "fp8blk_gated_linear_w8a16": (_st, _gated_linear_args),
+    "fp8blk_gated_linear_w8a8": (_st, _gated_linear_args),
+    "fp8blk_gated_backward": (_st, [_p, _i64, _p, _p, _i64, _i32, _p, _i64, _i64, _i64, _p]),
+    "fp8blk_epilogue_backward": (_st, [_p, _i64, _p, _i64, _i32, _p, _i64, _p, _i64, _i64, _p, _sz, _p]),
+    "fp8blk_epilogue_backward_workspace_size": (_sz, [_i64, _i64]),
+    "fp8blk_transpose_weight": (_st, [_p, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _i32, _p]),
+    "fp8blk_linear_grad_weight": (_st, [_p, _i64, _p, _i64, _p, _i64, _i32, _i32, _i64, _i64, _i64, _p]),
     "fp8blk_encode_e4m3": (_st, [_p, _i64, _p, _p]),
     "fp8blk_read_device_error": (_st, [ctypes.POINTER(ctypes.c_uint32)]),
     "fp8blk_selftest_wait_timeout": (_st, [_i64, _p]),
@@ -269,6 +297,285 @@ def streamed_linears(jobs, slots, slot_bytes: int, nslots: int, workspace, compu
     _check(lib().fp8blk_streamed_linears(arr, len(jobs), slots.data_ptr(), slot_bytes, nslots,
                                          ws_ptr, ws_len, compute.cuda_stream, copy.cuda_stream, ev),
            "fp8blk_streamed_linears")
+
+
+# ------------------------------------------------- feed-forward operators
+def _matrix(t, shape, dtype, device, what):
+    """Checks a 2-D operand: dtype, shape, device; returns its leading dimension."""
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what}: on {t.device}, expected {device}")
+    return _ld(t)
+
+
+def _device(t, what):
+    """The device of the call's tensors: the current CUDA device, whose stream it uses."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what}: on {t.device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {name!r}: one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+def _dims(t, what):
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected a 2-D tensor")
+    return t.shape
+
+
+def _weight(q, s, N, K, device, what):
+    """Checks a block-FP8 weight; returns its codes' leading dimension."""
+    import torch
+    ld = _matrix(q, (N, K), torch.uint8, device, f"{what} codes")
+    if N and K and (tuple(s.shape) != (_cdiv(N, 128), _cdiv(K, 128)) or not s.is_contiguous()):
+        raise ValueError(f"{what} scales: expected a contiguous [{_cdiv(N, 128)}, {_cdiv(K, 128)}] grid")
+    if s.dtype != torch.float32 or s.device != device:
+        raise ValueError(f"{what} scales: expected float32 on {device}")
+    return ld
+
+
+def _scratch(workspace, need, device):
+    """(tensor kept alive, pointer, bytes) of a workspace, allocated here if None."""
+    import torch
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on {device}")
+    if workspace is None:
+        return None, None, 0
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _new(rows, cols, align, dtype, device):
+    return _padded(rows, cols, _round_up(max(cols, 1), align), dtype, device)
+
+
+def _linear_epilogue(mode, name, x, q, scale_inv, bias, activation, residual, preact, out, workspace):
+    import torch
+    act = _activation(activation)
+    bf16 = torch.bfloat16
+    M, K = _dims(x, "x")
+    N = _dims(q, "q")[0]
+    dev = _device(x, "x")
+    ldx = _matrix(x, (M, K), bf16, dev, "x")
+    ldq = _weight(q, scale_inv, N, K, dev, "weight")
+    ep = Epilogue(None, act, None, 0, None, 0)
+    if bias is not None:
+        if tuple(bias.shape) != (N,) or bias.dtype != bf16 or not bias.is_contiguous() or bias.device != dev:
+            raise ValueError(f"bias: expected {N} contiguous BF16 values on {dev}")
+        ep.bias = bias.data_ptr()
+    if residual is not None:
+        ep.residual, ep.ldr = residual.data_ptr(), _matrix(residual, (M, N), bf16, dev, "residual")
+    if preact is not None:
+        ep.preact, ep.ldp = preact.data_ptr(), _matrix(preact, (M, N), bf16, dev, "preact")
+    if out is None:
+        out = _new(M, N, 8, bf16, dev)
+    ldy = _matrix(out, (M, N), bf16, dev, "out")
+    workspace, ws, ws_len = _scratch(workspace, workspace_size(mode, M, N, K), dev)
+    _check(getattr(lib(), name)(x.data_ptr(), ldx, q.data_ptr(), ldq, scale_inv.data_ptr(),
+                                out.data_ptr(), ldy, M, N, K, ctypes.byref(ep), ws, ws_len,
+                                _stream()), name)
+    return out
+
+
+def linear_w8a16_epilogue(x, q, scale_inv, bias=None, activation="none", residual=None, preact=None,
+                          out=None, workspace=None):
+    """y = act(x . dequant(W)^T + bias) + residual, BF16 activations; y BF16 [M, N].
+
+    bias BF16 [N]; residual BF16 [M, N], which out may be itself; preact BF16
+    [M, N] receives z = x . dequant(W)^T + bias for epilogue_backward."""
+    return _linear_epilogue(0, "fp8blk_linear_w8a16_epilogue", x, q, scale_inv, bias, activation,
+                            residual, preact, out, workspace)
+
+
+def linear_w8a8_epilogue(x, q, scale_inv, bias=None, activation="none", residual=None, preact=None,
+                         out=None, workspace=None):
+    """linear_w8a16_epilogue with x quantized per 1x128 K-group to E4M3."""
+    return _linear_epilogue(1, "fp8blk_linear_w8a8_epilogue", x, q, scale_inv, bias, activation,
+                            residual, preact, out, workspace)
+
+
+def _gated_linear(mode, name, x, q_gate, s_gate, q_up, s_up, activation, out, preact, workspace):
+    import torch
+    act = _activation(activation)
+    bf16 = torch.bfloat16
+    M, K = _dims(x, "x")
+    N = _dims(q_gate, "q_gate")[0]
+    dev = _device(x, "x")
+    ldx = _matrix(x, (M, K), bf16, dev, "x")
+    ldq = _weight(q_gate, s_gate, N, K, dev, "gate weight")
+    if _weight(q_up, s_up, N, K, dev, "up weight") != ldq:
+        raise ValueError("q_gate and q_up: expected one row stride")
+    g = u = None
+    ldgu = 0
+    if preact is not None:
+        g, u = preact
+        ldgu = _matrix(g, (M, N), bf16, dev, "g")
+        if _matrix(u, (M, N), bf16, dev, "u") != ldgu:
+            raise ValueError("g and u: expected one row stride")
+    if out is None:
+        out = _new(M, N, 8, bf16, dev)
+    ldh = _matrix(out, (M, N), bf16, dev, "out")
+    workspace, ws, ws_len = _scratch(workspace, workspace_size(mode, M, 2 * N, K), dev)
+    _check(getattr(lib(), name)(x.data_ptr(), ldx, q_gate.data_ptr(), s_gate.data_ptr(),
+                                q_up.data_ptr(), s_up.data_ptr(), ldq, act, out.data_ptr(), ldh,
+                                g.data_ptr() if g is not None else None,
+                                u.data_ptr() if u is not None else None, ldgu, M, N, K, ws, ws_len,
+                                _stream()), name)
+    return out
+
+
+def gated_linear_w8a16(x, q_gate, s_gate, q_up, s_up, activation="silu", out=None, preact=None,
+                       workspace=None):
+    """h = act(x . dequant(Wg)^T) * (x . dequant(Wu)^T), BF16 activations; h BF16 [M, N].
+
+    Both weights [N, K] with one row stride (a fused [2N, K] weight with
+    N % 128 == 0 is passed as its two halves). preact: a pair (g, u) of BF16
+    [M, N] with one row stride, which receive the two products for
+    gated_backward. The workspace is that of 2 N outputs."""
+    return _gated_linear(0, "fp8blk_gated_linear_w8a16", x, q_gate, s_gate, q_up, s_up, activation,
+                         out, preact, workspace)
+
+
+def gated_linear_w8a8(x, q_gate, s_gate, q_up, s_up, activation="silu", out=None, preact=None,
+                      workspace=None):
+    """gated_linear_w8a16 with x quantized per 1x128 K-group to E4M3."""
+    return _gated_linear(1, "fp8blk_gated_linear_w8a8", x, q_gate, s_gate, q_up, s_up, activation,
+                         out, preact, workspace)
+
+
+def gated_backward(dh, g, u, activation="silu", out=None):
+    """dgu BF16 [M, 2 Np], Np = round_up(N, 128): dg = dh u act'(g) in columns
+    [0, N), du = dh act(g) in [Np, Np + N), zeros between. dx is then
+    linear_w8a16(dgu, *transpose_gated_weights(...))."""
+    import torch
+    act = _activation(activation)
+    bf16 = torch.bfloat16
+    M, N = _dims(dh, "dh")
+    dev = _device(dh, "dh")
+    lddh = _matrix(dh, (M, N), bf16, dev, "dh")
+    ldgu = _matrix(g, (M, N), bf16, dev, "g")
+    if _matrix(u, (M, N), bf16, dev, "u") != ldgu:
+        raise ValueError("g and u: expected one row stride")
+    width = 2 * _round_up(N, 128)
+    if out is None:
+        out = torch.empty((M, width), dtype=bf16, device=dev)
+    ldo = _matrix(out, (M, width), bf16, dev, "out")
+    _check(lib().fp8blk_gated_backward(dh.data_ptr(), lddh, g.data_ptr(), u.data_ptr(), ldgu, act,
+                                       out.data_ptr(), ldo, M, N, _stream()), "fp8blk_gated_backward")
+    return out
+
+
+def epilogue_backward_workspace_size(M: int, N: int) -> int:
+    return int(lib().fp8blk_epilogue_backward_workspace_size(M, N))
+
+
+def epilogue_backward(dy, z=None, activation="none", dz=None, bias_grad=True, workspace=None):
+    """(dz, dbias): dz = dy act'(z) in BF16, dbias float32 [N] its column sums
+    before rounding (None without bias_grad). z is the kept preact (not needed
+    for "none", whose dz is dy itself unless a dz is given). dz may be dy or z."""
+    import torch
+    act = _activation(activation)
+    bf16 = torch.bfloat16
+    M, N = _dims(dy, "dy")
+    dev = _device(dy, "dy")
+    lddy = _matrix(dy, (M, N), bf16, dev, "dy")
+    ldz = 0
+    if z is not None:
+        ldz = _matrix(z, (M, N), bf16, dev, "z")
+    elif act != 0:
+        raise ValueError("z: needed for every activation but none")
+    if dz is None:
+        dz = dy if act == 0 else _new(M, N, 8, bf16, dev)
+    lddz = _matrix(dz, (M, N), bf16, dev, "dz")
+    dbias = torch.empty(N, dtype=torch.float32, device=dev) if bias_grad else None
+    need = epilogue_backward_workspace_size(M, N) if bias_grad else 0
+    workspace, ws, ws_len = _scratch(workspace, need, dev)
+    _check(lib().fp8blk_epilogue_backward(dy.data_ptr(), lddy, z.data_ptr() if z is not None else None,
+                                          ldz, act, dz.data_ptr(), lddz,
+                                          dbias.data_ptr() if bias_grad else None, M, N, ws, ws_len,
+                                          _stream()), "fp8blk_epilogue_backward")
+    return dz, dbias
+
+
+def _transpose_into(q, s, qt, st, zero_pad):
+    N, K = q.shape
+    _check(lib().fp8blk_transpose_weight(q.data_ptr(), _ld(q), s.data_ptr(), N, K, qt.data_ptr(),
+                                         _ld(qt), st.data_ptr(), _ld(st), zero_pad, _stream()),
+           "fp8blk_transpose_weight")
+
+
+def transpose_weight(q, scale_inv, qt=None, st=None):
+    """(qt, st): the transposed block-FP8 weight, codes [K, N] and scales
+    [ceil(K/128), ceil(N/128)], exact. dx = linear_w8a16(dz, qt, st)."""
+    import torch
+    N, K = _dims(q, "q")
+    dev = _device(q, "q")
+    _weight(q, scale_inv, N, K, dev, "weight")
+    if qt is None:
+        qt = _new(K, N, 16, torch.uint8, dev)
+    if st is None:
+        st = torch.empty((_cdiv(K, 128), _cdiv(N, 128)), dtype=torch.float32, device=dev)
+    _weight(qt, st, K, N, dev, "transposed weight")
+    _transpose_into(q, scale_inv, qt, st, 0)
+    return qt, st
+
+
+def transpose_gated_weights(q_gate, s_gate, q_up, s_up, qt=None, st=None):
+    """(qt, st): both transposed weights of a gated linear side by side, codes
+    [K, 2 Np] (Np = round_up(N, 128), zero codes between), the layout that
+    gated_backward's output multiplies."""
+    import torch
+    N, K = _dims(q_gate, "q_gate")
+    dev = _device(q_gate, "q_gate")
+    _weight(q_gate, s_gate, N, K, dev, "gate weight")
+    _weight(q_up, s_up, N, K, dev, "up weight")
+    NB = _cdiv(N, 128)
+    Np = 128 * NB
+    if qt is None:
+        qt = torch.empty((K, 2 * Np), dtype=torch.uint8, device=dev)
+    if st is None:
+        st = torch.empty((_cdiv(K, 128), 2 * NB), dtype=torch.float32, device=dev)
+    _weight(qt, st, K, 2 * Np, dev, "transposed weight")
+    for i, (q, s) in enumerate(((q_gate, s_gate), (q_up, s_up))):
+        _transpose_into(q, s, qt[:, i * Np:(i + 1) * Np], st[:, i * NB:(i + 1) * NB], 1)
+    return qt, st
+
+
+def linear_grad_weight(dz, x, out=None, accumulate=False, dtype=None):
+    """dw [N, K] = dz^T . x over the tokens of dz BF16 [M, N] and x BF16 [M, K],
+    FP32 sums; float32 unless out or dtype says BF16. accumulate adds to a
+    float32 out."""
+    import torch
+    bf16, f32 = torch.bfloat16, torch.float32
+    M, N = _dims(dz, "dz")
+    K = _dims(x, "x")[1]
+    dev = _device(dz, "dz")
+    lddz = _matrix(dz, (M, N), bf16, dev, "dz")
+    ldx = _matrix(x, (M, K), bf16, dev, "x")
+    dtype = dtype or (out.dtype if out is not None else f32)
+    if dtype not in (bf16, f32):
+        raise ValueError(f"dw: expected float32 or bfloat16, got {dtype}")
+    if accumulate and (out is None or dtype != f32):
+        raise ValueError("accumulate: needs a float32 out")
+    if out is None:
+        out = _new(N, K, 4 if dtype == f32 else 8, dtype, dev)
+    lddw = _matrix(out, (N, K), dtype, dev, "out")
+    _check(lib().fp8blk_linear_grad_weight(dz.data_ptr(), lddz, x.data_ptr(), ldx, out.data_ptr(), lddw,
+                                           int(dtype == f32), int(accumulate), M, N, K, _stream()),
+           "fp8blk_linear_grad_weight")
+    return out
 
 
 def encode_e4m3(v):

@@ -82,12 +82,6 @@ fp8blk_status make_launch(fp8blk_stream stream, Launch* L) {
   return FP8BLK_OK;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-fp8blk_status cuda_status(cudaError_t e) { return e == cudaSuccess ? FP8BLK_OK : FP8BLK_ERR_CUDA; }
-
-constexpr int64_t kInt32Max = 0x7FFFFFFFLL;
-
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -106,10 +100,6 @@ EncodeTiledFn encode_tiled_fn() {
   });
   return fn;
 }
-
-int64_t w8a8_ldqx(int64_t K) { return round_up(K, 16); }
-int64_t w8a8_ldsx(int64_t M) { return round_up(M, 128); }
-int64_t w8a8_sx_offset(int64_t M, int64_t K) { return round_up(M * w8a8_ldqx(K), 256); }
 
 }  // namespace
 

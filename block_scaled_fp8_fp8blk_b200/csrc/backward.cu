@@ -1,0 +1,329 @@
+// The memory-bound kernels of the backward passes: the gated product's and
+// the epilogue's derivative, and the transposed weight that turns dx = dz . W
+// into an ordinary linear.
+//
+// Each touches every byte once: 16-byte loads and stores along the rows,
+// enough of them in flight per SM to cover the latency of HBM, and nothing
+// kept between kernels but the column sums of the bias gradient.
+#include <cuda_runtime.h>
+
+#include "epilogue.cuh"
+#include "internal.cuh"
+#include "ptx.cuh"
+
+namespace fp8blk {
+namespace {
+
+// Eight BF16 values of a row from column c on: one 16-byte load where all
+// eight exist, else the existing ones and zeros.
+__device__ __forceinline__ void load8(const uint16_t* row, int64_t c, int64_t n, float (&v)[8]) {
+  if (c + 8 <= n) {
+    const uint4 w = *reinterpret_cast<const uint4*>(row + c);
+    v[0] = bf16_lo_to_f32(w.x), v[1] = bf16_hi_to_f32(w.x);
+    v[2] = bf16_lo_to_f32(w.y), v[3] = bf16_hi_to_f32(w.y);
+    v[4] = bf16_lo_to_f32(w.z), v[5] = bf16_hi_to_f32(w.z);
+    v[6] = bf16_lo_to_f32(w.w), v[7] = bf16_hi_to_f32(w.w);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < n ? bf16_bits_to_f32(row[c + i]) : 0.0f;
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(cvt_bf16x2(v[1], v[0]), cvt_bf16x2(v[3], v[2]), cvt_bf16x2(v[5], v[4]),
+                    cvt_bf16x2(v[7], v[6]));
+}
+
+// dg = dh u act'(g), du = dh act(g): eight columns per thread, rows in steps
+// of the grid. The columns between N and Np = round_up(N, 128) get zeros (the
+// loads give dh = 0 there).
+__global__ void __launch_bounds__(256)
+    gated_backward_kernel(const uint16_t* __restrict__ dh, int64_t lddh,
+                          const uint16_t* __restrict__ g, const uint16_t* __restrict__ u,
+                          int64_t ldgu, ActParams act, uint16_t* __restrict__ dgu, int64_t lddgu,
+                          int64_t M, int64_t N, int64_t Np) {
+  const int64_t c = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (c >= Np) return;
+  for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
+    float d[8], gv[8], uv[8];
+    load8(dh + m * lddh, c, N, d);
+    load8(g + m * ldgu, c, N, gv);
+    load8(u + m * ldgu, c, N, uv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a;
+      const float s = act_slope(act, gv[i], a);
+      gv[i] = d[i] * uv[i] * s;
+      uv[i] = d[i] * a;
+    }
+    uint16_t* out = dgu + m * lddgu + c;
+    *reinterpret_cast<uint4*>(out) = pack8(gv);
+    *reinterpret_cast<uint4*>(out + Np) = pack8(uv);
+  }
+}
+
+// dz = dy act'(z) and, with SUM, the column sums of the unrounded products. A
+// block takes 256 columns (32 lanes x 8) and a run of rows, eight at a time;
+// each thread sums its rows, the block adds its eight warps in order, and the
+// blocks of one column strip are added in order by column_sum_kernel. So the
+// order of the sum depends on the sizes alone. dz may be dy or z: a thread
+// writes only what it has read.
+constexpr int kStripCols = 256, kRowsPerStep = 8;
+
+template <bool SUM>
+__global__ void __launch_bounds__(256)
+    epilogue_backward_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz,
+                             ActParams act, uint16_t* dz, int64_t lddz, float* sums, int64_t M,
+                             int64_t N, int64_t rows) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * kStripCols + lane * 8;
+  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * rows;
+  const int64_t m1 = m0 + rows < M ? m0 + rows : M;
+  float sum[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
+  if (c < N) {
+#pragma unroll 2
+    for (int64_t m = m0 + warp; m < m1; m += kRowsPerStep) {
+      float d[8];
+      load8(dy + m * lddy, c, N, d);
+      if (z) {
+        float v[8];
+        load8(z + m * ldz, c, N, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float a;
+          d[i] *= act_slope(act, v[i], a);
+        }
+      }
+      if (dz) {
+        uint16_t* out = dz + m * lddz + c;
+        if (c + 8 <= N) {
+          *reinterpret_cast<uint4*>(out) = pack8(d);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < N) out[i] = static_cast<uint16_t>(cvt_bf16x2(0.0f, d[i]));
+        }
+      }
+      if constexpr (SUM) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += d[i];
+      }
+    }
+  }
+  if constexpr (SUM) {
+    __shared__ float s[8][kStripCols];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[warp][lane * 8 + i] = sum[i];
+    __syncthreads();
+    const int64_t n = static_cast<int64_t>(blockIdx.x) * kStripCols + threadIdx.x;
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += s[w][threadIdx.x];
+    if (n < N) sums[static_cast<int64_t>(blockIdx.y) * N + n] = t;
+  }
+}
+
+__global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ parts,
+                                                         int64_t splits, int64_t N,
+                                                         float* __restrict__ out) {
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (n >= N) return;
+  float t = 0.0f;
+#pragma unroll 4
+  for (int64_t i = 0; i < splits; ++i) t += parts[i * N + n];
+  out[n] = t;
+}
+
+// Row runs of epilogue_backward_kernel: enough blocks to fill the machine four
+// times (4 x 148), whole steps of eight rows each.
+struct RowSplit {
+  int64_t rows, splits;
+};
+RowSplit row_split(int64_t M, int64_t N) {
+  const int64_t strips = cdiv(N, kStripCols), want = cdiv(592, strips);
+  const int64_t rows = round_up(cdiv(M, want), kRowsPerStep);
+  return {rows, cdiv(M, rows)};
+}
+
+// qt[k][n] = q[n][k] for one 128 x 128 block of codes per thread block. A
+// thread transposes 4 x 4 codes in registers; the words cross through shared
+// memory, word (k, n/4) at column (n/4) ^ (k/4): both the writes (lanes along
+// k/4) and the reads (lanes along n/4) then touch 32 different banks. Rows are
+// read and written as whole 128-byte lines.
+__global__ void __launch_bounds__(256)
+    transpose_kernel(const uint8_t* __restrict__ q, int64_t ldq, const float* __restrict__ s,
+                     int64_t N, int64_t K, uint8_t* __restrict__ qt, int64_t ldqt,
+                     float* __restrict__ st, int64_t ldst, int64_t n_end) {
+  __shared__ uint32_t t[128 * 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t kb = blockIdx.x, nb = blockIdx.y;
+  const int64_t k0 = kb * 128, n0 = nb * 128, k = k0 + 4 * lane;
+  uint32_t w[4][4];
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t n = n0 + 4 * (warp + 8 * b) + i;
+      uint32_t v = 0;
+      if (n < N) {
+        const uint8_t* p = q + n * ldq + k;
+        if (k + 4 <= K) {
+          v = *reinterpret_cast<const uint32_t*>(p);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (k + e < K) v |= static_cast<uint32_t>(p[e]) << (8 * e);
+        }
+      }
+      w[b][i] = v;
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    // 16-bit halves, then bytes: o[e] = byte e of the four rows.
+    const uint32_t a = __byte_perm(w[b][0], w[b][1], 0x5140);  // (0: b0 b1 interleaved) e = 0, 1
+    const uint32_t c = __byte_perm(w[b][2], w[b][3], 0x5140);
+    const uint32_t d = __byte_perm(w[b][0], w[b][1], 0x7362);  // e = 2, 3
+    const uint32_t f = __byte_perm(w[b][2], w[b][3], 0x7362);
+    const int col = (warp + 8 * b) ^ lane;
+    t[(4 * lane + 0) * 32 + col] = __byte_perm(a, c, 0x5410);
+    t[(4 * lane + 1) * 32 + col] = __byte_perm(a, c, 0x7632);
+    t[(4 * lane + 2) * 32 + col] = __byte_perm(d, f, 0x5410);
+    t[(4 * lane + 3) * 32 + col] = __byte_perm(d, f, 0x7632);
+  }
+  __syncthreads();
+  const int64_t n = n0 + 4 * lane;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int kk = warp + 8 * i;
+    if (k0 + kk >= K) break;
+    const uint32_t v = t[kk * 32 + (lane ^ (kk >> 2))];
+    uint8_t* p = qt + (k0 + kk) * ldqt + n;
+    if (n + 4 <= n_end) {
+      *reinterpret_cast<uint32_t*>(p) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < n_end) p[e] = static_cast<uint8_t>(v >> (8 * e));
+    }
+  }
+  if (threadIdx.x == 0) st[kb * ldst + nb] = s[nb * gridDim.x + kb];
+}
+
+}  // namespace
+}  // namespace fp8blk
+
+using namespace fp8blk;
+
+extern "C" {
+
+fp8blk_status fp8blk_gated_backward(const void* dh, int64_t lddh, const void* g, const void* u,
+                                    int64_t ldgu, int32_t activation, void* dgu, int64_t lddgu,
+                                    int64_t M, int64_t N, fp8blk_stream stream) {
+  if (!valid_activation(activation) || M < 0 || N < 0) return FP8BLK_ERR_INVALID_ARG;
+  if (M == 0 || N == 0) return FP8BLK_OK;
+  if (M > kInt32Max || N > kInt32Max) return FP8BLK_ERR_INVALID_ARG;
+  const int64_t Np = round_up(N, 128);
+  if (!dh || !g || !u || !dgu || lddh < N || ldgu < N || lddgu < 2 * Np) return FP8BLK_ERR_INVALID_ARG;
+  if (lddh % 8 || ldgu % 8 || lddgu % 8 || !aligned(dh, 16) || !aligned(g, 16) || !aligned(u, 16) ||
+      !aligned(dgu, 16))
+    return FP8BLK_ERR_ALIGNMENT;
+  Launch L;
+  fp8blk_status st = current_launch(stream, &L);
+  if (st != FP8BLK_OK) return st;
+  const int64_t gx = cdiv(Np, 8 * 256);
+  // Rows in steps of gridDim.y: at most 16 blocks per SM in all.
+  const int64_t gy_max = cdiv(16 * L.num_sms, gx);
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(M < gy_max ? M : gy_max));
+  gated_backward_kernel<<<grid, 256, 0, L.stream>>>(
+      static_cast<const uint16_t*>(dh), lddh, static_cast<const uint16_t*>(g),
+      static_cast<const uint16_t*>(u), ldgu, act_params(activation), static_cast<uint16_t*>(dgu),
+      lddgu, M, N, Np);
+  return cuda_status(cudaGetLastError());
+}
+
+size_t fp8blk_epilogue_backward_workspace_size(int64_t M, int64_t N) {
+  if (M <= 0 || N <= 0) return 0;
+  const RowSplit r = row_split(M, N);
+  return r.splits > 1 ? static_cast<size_t>(r.splits) * static_cast<size_t>(N) * sizeof(float) : 0;
+}
+
+fp8blk_status fp8blk_epilogue_backward(const void* dy, int64_t lddy, const void* z, int64_t ldz,
+                                       int32_t activation, void* dz, int64_t lddz, float* dbias,
+                                       int64_t M, int64_t N, void* workspace,
+                                       size_t workspace_bytes, fp8blk_stream stream) {
+  if (!valid_activation(activation) || M < 0 || N < 0) return FP8BLK_ERR_INVALID_ARG;
+  if (M > kInt32Max || N > kInt32Max) return FP8BLK_ERR_INVALID_ARG;
+  if (N == 0 || (M == 0 && !dbias)) return FP8BLK_OK;
+  if (!aligned(dbias, 4)) return FP8BLK_ERR_ALIGNMENT;
+  const bool identity = activation == FP8BLK_ACT_NONE;
+  if (M > 0) {
+    if (!dy || lddy < N || (!identity && !z)) return FP8BLK_ERR_INVALID_ARG;
+    if (lddy % 8 || !aligned(dy, 16)) return FP8BLK_ERR_ALIGNMENT;
+    if (!identity) {
+      if (ldz < N) return FP8BLK_ERR_INVALID_ARG;
+      if (ldz % 8 || !aligned(z, 16)) return FP8BLK_ERR_ALIGNMENT;
+    }
+    if (dz) {
+      if (lddz < N || (dz == dy && lddz != lddy) || (dz == z && !identity && lddz != ldz))
+        return FP8BLK_ERR_INVALID_ARG;
+      if (lddz % 8 || !aligned(dz, 16)) return FP8BLK_ERR_ALIGNMENT;
+    }
+    if (dbias) {
+      const size_t need = fp8blk_epilogue_backward_workspace_size(M, N);
+      if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 256)))
+        return FP8BLK_ERR_WORKSPACE;
+    }
+  }
+  if (identity && dz == dy) dz = nullptr;  // already there
+  if (M > 0 && !dz && !dbias) return FP8BLK_OK;
+  Launch L;
+  fp8blk_status st = current_launch(stream, &L);
+  if (st != FP8BLK_OK) return st;
+  if (M == 0)
+    return cuda_status(cudaMemsetAsync(dbias, 0, static_cast<size_t>(N) * sizeof(float), L.stream));
+  const RowSplit r = row_split(M, N);
+  if (r.splits > 65535) return FP8BLK_ERR_INVALID_ARG;  // (592 at most)
+  const dim3 grid(static_cast<unsigned>(cdiv(N, kStripCols)), static_cast<unsigned>(r.splits));
+  const uint16_t* dyp = static_cast<const uint16_t*>(dy);
+  const uint16_t* zp = identity ? nullptr : static_cast<const uint16_t*>(z);
+  uint16_t* dzp = static_cast<uint16_t*>(dz);
+  const ActParams act = act_params(activation);
+  if (!dbias) {
+    epilogue_backward_kernel<false><<<grid, 256, 0, L.stream>>>(dyp, lddy, zp, ldz, act, dzp, lddz,
+                                                                nullptr, M, N, r.rows);
+    return cuda_status(cudaGetLastError());
+  }
+  float* sums = r.splits > 1 ? static_cast<float*>(workspace) : dbias;
+  epilogue_backward_kernel<true><<<grid, 256, 0, L.stream>>>(dyp, lddy, zp, ldz, act, dzp, lddz,
+                                                             sums, M, N, r.rows);
+  if (cudaGetLastError() != cudaSuccess) return FP8BLK_ERR_CUDA;
+  if (r.splits > 1)
+    column_sum_kernel<<<static_cast<unsigned>(cdiv(N, 256)), 256, 0, L.stream>>>(sums, r.splits, N, dbias);
+  return cuda_status(cudaGetLastError());
+}
+
+fp8blk_status fp8blk_transpose_weight(const uint8_t* q, int64_t ldq, const float* scale_inv,
+                                      int64_t N, int64_t K, uint8_t* qt, int64_t ldqt, float* st,
+                                      int64_t ldst, int32_t zero_pad, fp8blk_stream stream) {
+  if (N < 0 || K < 0 || (zero_pad != 0 && zero_pad != 1)) return FP8BLK_ERR_INVALID_ARG;
+  if (N == 0 || K == 0) return FP8BLK_OK;
+  const int64_t n_end = zero_pad ? round_up(N, 128) : N;
+  if (!q || !scale_inv || !qt || !st || ldq < K || ldqt < n_end || ldst < cdiv(N, 128))
+    return FP8BLK_ERR_INVALID_ARG;
+  // Grid limits: blocks of K along x, of N along y.
+  if (cdiv(K, 128) > kInt32Max || cdiv(N, 128) > 65535) return FP8BLK_ERR_INVALID_ARG;
+  if (ldq % 16 || ldqt % 16 || !aligned(q, 16) || !aligned(qt, 16) || !aligned(scale_inv, 4) ||
+      !aligned(st, 4))
+    return FP8BLK_ERR_ALIGNMENT;
+  Launch L;
+  fp8blk_status status = current_launch(stream, &L);
+  if (status != FP8BLK_OK) return status;
+  const dim3 grid(static_cast<unsigned>(cdiv(K, 128)), static_cast<unsigned>(cdiv(N, 128)));
+  transpose_kernel<<<grid, 256, 0, L.stream>>>(q, ldq, scale_inv, N, K, qt, ldqt, st, ldst, n_end);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -1,0 +1,436 @@
+// Weight gradient of a linear on tcgen05:
+//   dw[n][k] = sum_m dz[m][n] * x[m][k]     (BF16 x BF16, FP32 sums).
+//
+// The contraction runs over the tokens, the rows of both operands, so both
+// are "MN-major" to the tensor cores: their contiguous dimension is the
+// output's. TMA brings boxes of 64 tokens x 64 columns (128 bytes, 128-byte
+// swizzle) and the MMA descriptors name that order, so nothing is transposed.
+// Tokens past M are zero-filled by TMA in both operands.
+//
+// What bounds it is the tensor pipe, if the operands arrive: a 128 x 256 tile
+// on one SM would load 48 KB per 512 MMA cycles, 96 bytes per clock and SM,
+// about what L2 can deliver. So two SMs (a cluster of two CTAs, cta_group::2)
+// share a 256 x 256 tile: each loads its 128 rows of dz^T and its 128 columns
+// of x (32 KB per 64 tokens, 64 bytes per clock), holds its 128 output rows in
+// TMEM, and the pair's MMA (M = 256, N = 256, K = 16) reads the operands of
+// both. The accumulator is double-buffered (2 x 256 of the 512 TMEM columns),
+// so a tile's stores overlap the next tile's products.
+//
+// Roles per CTA (12 warps):
+//   warp 0   lanes 0, 1: TMA producers of the two 64-column boxes of dz;
+//   warp 1   lanes 0, 1: of x. Loads of both CTAs complete on the stage's
+//            barrier in the leader (CTA rank 0 of the pair);
+//   warp 2   leader: MMA issuer; both: TMEM allocation;
+//   warps 4-11  epilogue: warp 4 + 4h + q owns TMEM lane quadrant q and
+//            columns [128h, 128h + 128) of its CTA's 128 x 256 accumulator.
+// A commit stalls its issuer for a few hundred cycles, so stages are released
+// in pairs: one commit per 8 MMAs (1024 cycles of the pair's tensor pipes).
+// Every wait is bounded (kWaitLimitCycles) and reports to the error word.
+#include <cuda_bf16.h>
+
+#include <cstring>
+
+#include "internal.cuh"
+#include "ptx.cuh"
+
+namespace fp8blk {
+namespace {
+
+struct GradCfg {
+  static constexpr int BT = 64;                    // tokens per stage
+  static constexpr int TILE = 256;                 // output rows and columns of a pair's tile
+  static constexpr int BOX_BYTES = BT * 128;       // 64 tokens x 64 BF16
+  static constexpr int OP_BYTES = 2 * BOX_BYTES;   // one operand's 128 columns
+  static constexpr int STAGE_BYTES = 2 * OP_BYTES; // both operands of this CTA
+  static constexpr int ST = 6;                     // stages, released two at a time
+  static constexpr int PAIRS = ST / 2;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int THREADS = 128 + 32 * EPI_WARPS;
+  static constexpr int OUT_BYTES = 32 * 128;       // per epilogue warp: 32 rows x 128 B
+  static constexpr int NBAR = ST + PAIRS + 4;
+  static constexpr size_t SMEM_TILES =
+      static_cast<size_t>(ST) * STAGE_BYTES + static_cast<size_t>(EPI_WARPS) * OUT_BYTES;
+  static constexpr size_t SMEM = 1024 + SMEM_TILES + 8 * NBAR + 16;
+  // Both operands MN-major (bits 15 and 16).
+  static constexpr uint32_t IDESC = make_idesc(1u, 1u, 256, 256) | (1u << 15) | (1u << 16);
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(ST % 2 == 0, "stages are released in pairs");
+};
+
+// ------------------------------------------------------- CTA-pair instructions
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+// The address, in the cluster's shared window, of the given CTA's copy of p.
+__device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Orders later reads after what the peer CTA released with its arrivals.
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
+// 2-D tile load into this CTA's shared memory, counted on a barrier of the
+// pair (own or peer's; an address in the cluster's shared window).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar,
+                                                 int32_t c0, int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+      ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_addr(dst_smem)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+// One arrival on the barrier at this offset in both CTAs of the pair when all
+// MMAs issued so far by this thread have completed.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(smem_addr(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// D[tmem of both] (+)= A * B, A and B in the shared memory of both CTAs.
+__device__ __forceinline__ void mma_f16_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Tile store that adds to what is there (FP32).
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, const void* src, int32_t c0,
+                                           int32_t c1) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_addr(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+
+// Descriptor of an MN-major operand tile: boxes of 64 columns (128 bytes,
+// 128-byte swizzle) x BT tokens. Eight tokens are one 1024-byte swizzle atom
+// (stride byte offset); the next 64 columns are one box further (leading byte
+// offset). Sixteen tokens (one MMA's K) advance the start address by 2048.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(GradCfg::BOX_BYTES >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+template <bool FP32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradCfg::THREADS, 1)
+    grad_weight_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                       const __grid_constant__ CUtensorMap tm_w, void* __restrict__ dw, int64_t lddw,
+                       int N, int K, int k_tma, int steps, int ktiles, int tiles, int gk,
+                       int accumulate, unsigned* __restrict__ err) {
+  using C = GradCfg;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;                 // ST stages: dz (two boxes), x (two boxes)
+  uint8_t* sOut = smem + C::ST * C::STAGE_BYTES;  // EPI_WARPS x 4 KB staging
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::SMEM_TILES);
+  uint64_t* full = bars;                // leader: stage landed in both CTAs (4 arrivals + tx)
+  uint64_t* empty = full + C::ST;       // stage pair read by the MMAs       (1 commit)
+  uint64_t* acc_full = empty + C::PAIRS;  // accumulator complete            (1 commit)
+  uint64_t* acc_empty = acc_full + 2;     // leader: accumulator read        (16 epilogue warps)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
+  const int ntiles_n = tiles / ktiles;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::ST; ++s) mbar_init(&full[s], 4);
+    for (int p = 0; p < C::PAIRS; ++p) mbar_init(&empty[p], 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * C::EPI_WARPS);
+    }
+    mbar_init_fence();
+  }
+  if (warp == 2) tmem_alloc_pair(tmem_slot, 512);
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers and TMEM exist
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 2) {
+    if (lane < 2) {
+      // ------------------------------------------------------- producers
+      const CUtensorMap* map = warp == 0 ? &tm_a : &tm_b;
+      uint8_t* dst = smem + warp * C::OP_BYTES + lane * C::BOX_BYTES;
+      const uint32_t full0 = map_to_rank(full, 0);
+      tma_prefetch_map(map);
+      int j = 0;
+      bool ok = true;
+      for (int tile = pair; tile < tiles && ok; tile += npairs) {
+        int kt, nt;
+        tile_coords(tile, ktiles, ntiles_n, gk, kt, nt);
+        const int col = (warp == 0 ? nt : kt) * C::TILE + static_cast<int>(rank) * 128 + lane * 64;
+        for (int s = 0; s < steps; ++s, ++j) {
+          const int stage = j % C::ST;
+          if ((stage & 1) == 0 && j >= C::ST) {  // the pair's last use has been read
+            if (!mbar_wait(&empty[stage >> 1], static_cast<uint32_t>((j / C::ST - 1) & 1), err,
+                           kErrWaitLoad)) {
+              ok = false;
+              break;
+            }
+          }
+          // The leader's barrier counts this box and the peer's.
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::BOX_BYTES);
+          tma_load_2d_pair(dst + stage * C::STAGE_BYTES, map, full0 + 8u * stage, col, s * C::BT);
+        }
+      }
+      // Drain: the leader waits until the last stages have landed in both
+      // CTAs; the peer is kept alive by the cluster barrier at the end.
+      if (rank == 0)
+        for (int jj = (j > C::ST ? j - C::ST : 0); jj < j; ++jj)
+          mbar_wait(&full[jj % C::ST], static_cast<uint32_t>((jj / C::ST) & 1), err, kErrWaitLoad);
+    }
+  } else if (warp == 2) {
+    if (rank == 0 && lane == 0) {
+      // ------------------------------------------------------ MMA issuer
+      const uint64_t a0 = sw128_mnmajor_desc(smem_addr(smem));
+      const uint64_t b0 = sw128_mnmajor_desc(smem_addr(smem + C::OP_BYTES));
+      int j = 0, it = 0;
+      bool ok = true;
+      for (int tile = pair; tile < tiles && ok; tile += npairs, ++it) {
+        const int buf = it & 1;
+        if (it >= 2) {
+          if (!mbar_wait(&acc_empty[buf], static_cast<uint32_t>(((it >> 1) - 1) & 1), err, kErrWaitMma)) break;
+          fence_cluster();
+          tc_fence_after_sync();
+        }
+        const uint32_t d = tmem + static_cast<uint32_t>(buf * C::TILE);
+        for (int s = 0; s < steps; ++s, ++j) {
+          const int stage = j % C::ST;
+          if (!mbar_wait(&full[stage], static_cast<uint32_t>((j / C::ST) & 1), err, kErrWaitMma)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint64_t off = static_cast<uint64_t>((stage * C::STAGE_BYTES) >> 4);
+#pragma unroll
+          for (int q = 0; q < C::BT / 16; ++q)
+            mma_f16_ss_pair(d, a0 + off + (2048u >> 4) * q, b0 + off + (2048u >> 4) * q, C::IDESC,
+                            s > 0 || q > 0 ? 1u : 0u);
+          if (stage & 1) tc_commit_pair(&empty[stage >> 1]);
+        }
+        if (ok) tc_commit_pair(&acc_full[buf]);
+      }
+      // Drain: all MMAs complete before TMEM is released and either CTA
+      // leaves (the last accumulator's commit is the last one).
+      if (it > 0 && ok)
+        mbar_wait(&acc_full[(it - 1) & 1], static_cast<uint32_t>(((it - 1) >> 1) & 1), err, kErrWaitMma);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue
+    const int ew = warp - 4, quad = warp & 3, h = ew >> 2;
+    uint8_t* stage = sOut + ew * C::OUT_BYTES;
+    uint8_t* srow = stage + lane * 128;
+    const uint32_t acc_empty0 = map_to_rank(acc_empty, 0);
+    constexpr int CW = FP32 ? 32 : 64;       // columns of a 128-byte staging row
+    constexpr int EPC = FP32 ? 4 : 8;        // elements of a 16-byte chunk
+    int it = 0;
+    for (int tile = pair; tile < tiles; tile += npairs, ++it) {
+      int kt, nt;
+      tile_coords(tile, ktiles, ntiles_n, gk, kt, nt);
+      const int buf = it & 1;
+      if (!mbar_wait_warp(&acc_full[buf], static_cast<uint32_t>((it >> 1) & 1), err, kErrWaitEpilogue)) break;
+      tc_fence_after_sync();
+      const uint32_t t = tmem + (static_cast<uint32_t>(quad * 32) << 16) +
+                         static_cast<uint32_t>(buf * C::TILE + 128 * h);
+      const int r0 = nt * C::TILE + static_cast<int>(rank) * 128 + quad * 32;  // first output row
+      const int n = r0 + lane;
+#pragma unroll 1
+      for (int c0 = 0; c0 < 128; c0 += CW) {
+        const int base = kt * C::TILE + 128 * h + c0;  // first output column
+        uint32_t p[32];
+        uint4 o[8];
+        tmem_ld32x32(t + static_cast<uint32_t>(c0), p);
+        if constexpr (FP32) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) o[c] = make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+        } else {
+          auto f = [&](int i) { return cvt_bf16x2(__uint_as_float(p[2 * i + 1]), __uint_as_float(p[2 * i])); };
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[c] = make_uint4(f(4 * c), f(4 * c + 1), f(4 * c + 2), f(4 * c + 3));
+          tmem_ld32x32(t + static_cast<uint32_t>(c0 + 32), p);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[4 + c] = make_uint4(f(4 * c), f(4 * c + 1), f(4 * c + 2), f(4 * c + 3));
+        }
+        if (c0 + CW == 128) {  // the accumulator has been read
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc_empty0 + 8u * buf);
+        }
+        if (lane == 0) tma_store_wait_read<0>();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(srow + ((c ^ (lane & 7)) << 4)) = o[c];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && r0 < N && base < k_tma) {
+          if (FP32 && accumulate)
+            tma_add_2d(&tm_w, stage, base, r0);
+          else
+            tma_store_2d(&tm_w, stage, base, r0);
+          tma_store_commit();
+        }
+        // The columns of a ragged K past the last whole 16 bytes.
+        if (k_tma < K && k_tma >= base && k_tma < base + CW && n < N) {
+          const uint8_t* src = srow + ((((k_tma - base) / EPC) ^ (lane & 7)) << 4);
+          const int64_t at = static_cast<int64_t>(n) * lddw + k_tma;
+          for (int e = 0; e < K - k_tma; ++e) {
+            if constexpr (FP32) {
+              float* w = static_cast<float*>(dw) + at + e;
+              const float v = reinterpret_cast<const float*>(src)[e];
+              *w = accumulate ? *w + v : v;
+            } else {
+              static_cast<uint16_t*>(dw)[at + e] = reinterpret_cast<const uint16_t*>(src)[e];
+            }
+          }
+        }
+      }
+    }
+    if (lane == 0) tma_store_wait_all();
+  }
+
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may still signal it or read it
+  if (warp == 2) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// Pairs that can be resident at once (queried once per device and form).
+template <bool FP32>
+cudaError_t resident_pairs(int num_sms, int* pairs) {
+  static int known[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int n = __atomic_load_n(&known[dev], __ATOMIC_RELAXED);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(num_sms / 2 * 2));
+    cfg.blockDim = dim3(GradCfg::THREADS);
+    cfg.dynamicSmemBytes = GradCfg::SMEM;
+    e = cudaOccupancyMaxActiveClusters(&n, grad_weight_kernel<FP32>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    if (n > num_sms / 2) n = num_sms / 2;
+    __atomic_store_n(&known[dev], n, __ATOMIC_RELAXED);
+  }
+  *pairs = n;
+  return cudaSuccess;
+}
+
+// Output columns (x) whose operand columns a raster group may keep in L2.
+constexpr int64_t kRasterBytesGrad = 48ll << 20;
+
+template <bool FP32>
+cudaError_t launch_grad(const Launch& L, const uint16_t* dz, int64_t lddz, const uint16_t* x,
+                        int64_t ldx, void* dw, int64_t lddw, bool accumulate, int64_t M, int64_t N,
+                        int64_t K) {
+  using C = GradCfg;
+  CUtensorMap ta, tb, tw;
+  if (!make_tmap_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dz, N, M, 2 * lddz, 64, C::BT) ||
+      !make_tmap_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, K, M, 2 * ldx, 64, C::BT))
+    return cudaErrorInvalidValue;
+  constexpr int kEsz = FP32 ? 4 : 2;
+  const int64_t k_tma = K & ~int64_t{16 / kEsz - 1};  // whole 16-byte chunks
+  if (k_tma > 0) {
+    if (!make_tmap_2d(&tw, FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                      dw, k_tma, N, kEsz * lddw, 128 / kEsz, 32))
+      return cudaErrorInvalidValue;
+  } else {
+    memset(&tw, 0, sizeof(tw));
+  }
+  auto kern = grad_weight_kernel<FP32>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::SMEM);
+  if (e != cudaSuccess) return e;
+  int pairs = 0;
+  e = resident_pairs<FP32>(L.num_sms, &pairs);
+  if (e != cudaSuccess) return e;
+  const int64_t ktiles = cdiv(K, C::TILE), tiles = ktiles * cdiv(N, C::TILE), steps = cdiv(M, C::BT);
+  if (tiles * steps > 0x7FFFFFFFLL) return cudaErrorInvalidValue;  // 32-bit counters
+  if (tiles < pairs) pairs = static_cast<int>(tiles);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = L.stream;
+  return cudaLaunchKernelEx(&cfg, kern, ta, tb, tw, dw, lddw, static_cast<int>(N),
+                            static_cast<int>(K), static_cast<int>(k_tma), static_cast<int>(steps),
+                            static_cast<int>(ktiles), static_cast<int>(tiles),
+                            raster_group(ktiles, C::TILE * M * 2, kRasterBytesGrad),
+                            accumulate ? 1 : 0, L.err);
+}
+
+}  // namespace
+}  // namespace fp8blk
+
+using namespace fp8blk;
+
+extern "C" fp8blk_status fp8blk_linear_grad_weight(const void* dz, int64_t lddz, const void* x,
+                                                   int64_t ldx, void* dw, int64_t lddw,
+                                                   int32_t dw_fp32, int32_t accumulate, int64_t M,
+                                                   int64_t N, int64_t K, fp8blk_stream stream) {
+  if (M < 0 || N < 0 || K < 0) return FP8BLK_ERR_INVALID_ARG;
+  if ((dw_fp32 != 0 && dw_fp32 != 1) || (accumulate != 0 && accumulate != 1) ||
+      (accumulate && !dw_fp32))
+    return FP8BLK_ERR_INVALID_ARG;
+  if (N == 0 || K == 0) return FP8BLK_OK;
+  if (!dw || lddw < K || M > kInt32Max || N > kInt32Max || K > kInt32Max) return FP8BLK_ERR_INVALID_ARG;
+  if (lddw % (dw_fp32 ? 4 : 8) || !aligned(dw, 16)) return FP8BLK_ERR_ALIGNMENT;
+  if (M > 0) {
+    if (!dz || !x || lddz < N || ldx < K) return FP8BLK_ERR_INVALID_ARG;
+    if (lddz % 8 || ldx % 8 || !aligned(dz, 16) || !aligned(x, 16)) return FP8BLK_ERR_ALIGNMENT;
+  } else if (accumulate) {
+    return FP8BLK_OK;
+  }
+  Launch L;
+  fp8blk_status st = current_launch(stream, &L);
+  if (st != FP8BLK_OK) return st;
+  if (M == 0) {  // an empty sum
+    const size_t esz = dw_fp32 ? 4 : 2;
+    return cuda_status(cudaMemset2DAsync(dw, static_cast<size_t>(lddw) * esz, 0,
+                                         static_cast<size_t>(K) * esz, static_cast<size_t>(N), L.stream));
+  }
+  const uint16_t* a = static_cast<const uint16_t*>(dz);
+  const uint16_t* b = static_cast<const uint16_t*>(x);
+  return cuda_status(dw_fp32
+                         ? launch_grad<true>(L, a, lddz, b, ldx, dw, lddw, accumulate != 0, M, N, K)
+                         : launch_grad<false>(L, a, lddz, b, ldx, dw, lddw, false, M, N, K));
+}

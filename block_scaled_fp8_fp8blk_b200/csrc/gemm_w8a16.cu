@@ -40,15 +40,28 @@
 //                expand the odd slabs (the conversion is the per-slab cost
 //                at small token counts, so two groups overlap it).
 // Every wait is bounded (kWaitLimitCycles) and reports to the error word.
+//
+// EPI chooses what follows the sums (epilogue.cuh). A promotion thread holds
+// one weight row, i.e. one column of y, for a run of tokens, so kEpiFused has
+// one bias value per thread and reads the residual 16 tokens at a time, 64
+// contiguous bytes per warp and token, before it needs them. kEpiGated makes
+// each 128-row tile of 64 gate rows (TMEM lanes 0-63) and the 64 up rows of
+// the same outputs (lanes 64-127), so expansion, MMAs and promotion run as for
+// any weight; the two warps that hold g and u of the same outputs trade
+// halves of each 16-token group through shared memory (FP32) and each stores
+// act(g) * u of eight tokens. The split costs nothing per slab, where two
+// accumulators in one thread would have halved the tokens that share an
+// expansion. Split (stream-K) tiles get the same treatment in the fix-up.
 #include <cuda_bf16.h>
 
+#include "epilogue.cuh"
 #include "internal.cuh"
 #include "ptx.cuh"
 
 namespace fp8blk {
 namespace {
 
-template <int BT, int NSUB>
+template <int BT, int NSUB, int EPI>
 struct W8A16Cfg {
   static constexpr int Q_BYTES = 128 * 128;  // FP8 weight slab
   static constexpr int X_ATOM = BT * 128;    // BT rows x 64 BF16 (128 B)
@@ -73,8 +86,11 @@ struct W8A16Cfg {
   static constexpr int TMEM_P = 64 * AB;        // PB buffers x BT columns
   static constexpr int TMEM_USED = TMEM_P + PB * BT;
   static constexpr int TMEM_COLS = TMEM_USED <= 256 ? 256 : 512;
-  static constexpr int NBAR = 2 * QS + XS + AB + RD + PB * 2;
-  static constexpr int OUT_BYTES = 16 * 64;     // per epilogue warp: 16 tokens x 32 BF16
+  static constexpr int XW = EPI == kEpiGated ? 2 * NSUB : 0;  // gate/up warp pairs
+  static constexpr int NBAR = 2 * QS + XS + AB + RD + PB * 2 + XW;
+  // Per epilogue warp: 16 tokens x 32 BF16; gated: two buffers of 8 tokens x
+  // 32 FP32 for the trade, the idle one also staging the output.
+  static constexpr int OUT_BYTES = EPI == kEpiGated ? 2 * 8 * 128 : 16 * 64;
   static constexpr size_t SMEM_TILES = static_cast<size_t>(QS) * Q_BYTES +
                                        static_cast<size_t>(XS) * X_BYTES + 4 * NSUB * OUT_BYTES;
   static constexpr size_t SMEM = 1024 + SMEM_TILES + 8 * NBAR + 16;
@@ -240,13 +256,121 @@ __device__ __forceinline__ void tile_of(int t, int mtiles, int ntiles_total, int
   }
 }
 
-template <int BT, int NSUB, bool GROUPED>
+// ------------------------------------------------------------------- output
+// A warp holds 16 tokens x 32 columns of BF16 output staged as rows of 32
+// values: each lane stores 16 contiguous values (32 bytes) of one row.
+// ROWS = 8: 16 bytes per lane.
+template <int ROWS>
+__device__ __forceinline__ void flush_rows(const uint8_t* stg, uint16_t* out, int64_t ld, int m0,
+                                           int c_first, int M, int N, int lane) {
+  constexpr int LPR = 32 / ROWS;    // lanes per row
+  constexpr int VALS = 32 / LPR;    // values per lane
+  const int rr = lane / LPR, hh = lane % LPR;
+  const uint8_t* src = stg + rr * 64 + hh * VALS * 2;
+  const int m = m0 + rr, c0 = c_first + VALS * hh;
+  if (m < M && c0 < N) {
+    uint16_t* dst = out + static_cast<int64_t>(m) * ld + c0;
+    if (c0 + VALS <= N) {
+#pragma unroll
+      for (int i = 0; i < VALS / 8; ++i)
+        reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i];
+    } else {
+      for (int c = 0; c < N - c0; ++c) dst[c] = reinterpret_cast<const uint16_t*>(src)[c];
+    }
+  }
+  __syncwarp();  // the buffer may be written again
+}
+
+// Stages n tokens (n <= 16) of this lane's column and stores them.
+template <int ROWS>
+__device__ __forceinline__ void stage_and_flush(uint8_t* stg, const float* v, uint16_t* out,
+                                                int64_t ld, int m0, int c_first, int M, int N,
+                                                int lane) {
+#pragma unroll
+  for (int e = 0; e < ROWS; e += 2) {
+    const uint32_t b2 = cvt_bf16x2(v[e + 1], v[e]);
+    *reinterpret_cast<uint16_t*>(stg + e * 64 + lane * 2) = static_cast<uint16_t>(b2 & 0xFFFFu);
+    *reinterpret_cast<uint16_t*>(stg + (e + 1) * 64 + lane * 2) = static_cast<uint16_t>(b2 >> 16);
+  }
+  __syncwarp();
+  flush_rows<ROWS>(stg, out, ld, m0, c_first, M, N, lane);
+}
+
+// kEpiFused on 16 tokens m0.. of column n (this lane's; c_first its warp's
+// first column): z = v + bias, kept if asked, y = act(z) + residual.
+__device__ __forceinline__ void fused_group(const FusedEpi& e, float bias, float (&v)[16],
+                                            uint8_t* stg, uint16_t* y, int64_t ldy, int m0,
+                                            int c_first, int M, int N, int lane) {
+  const int n = c_first + lane;
+  uint16_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = 0;
+  if (e.residual && n < N) {
+    const uint16_t* rp = e.residual + static_cast<int64_t>(m0) * e.ldr + n;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (m0 + i < M) r[i] = rp[i * e.ldr];
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] += bias;
+  if (e.preact) stage_and_flush<16>(stg, v, e.preact, e.ldp, m0, c_first, M, N, lane);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = act_value(e.act, v[i]) + bf16_bits_to_f32(r[i]);
+  stage_and_flush<16>(stg, v, y, ldy, m0, c_first, M, N, lane);
+}
+
+// The trade between the warp that holds g and the warp that holds u of the
+// same 32 outputs (kEpiGated), 16 tokens at a time: each warp gives the half
+// that the other finishes (the gate's warp finishes tokens 0-7, the up's warp
+// 8-15), alternating between two buffers, with one barrier that both arrive on
+// and wait for. After a warp's wait for trade k, its partner has read trade
+// k - 1 (it read it before arriving for k), so the other buffer is free for
+// staging and then for trade k + 1.
+struct GateTrade {
+  uint8_t* mine;
+  uint8_t* theirs;
+  uint64_t* bar;
+  bool is_up;
+  int count = 0;
+};
+
+// act(g) * u of 16 tokens m0..; v holds g or u of this lane's column. Returns
+// false when the partner never arrived (a time-out, reported).
+__device__ __forceinline__ bool gated_group(GateTrade& t, const GatedEpi& e, float (&v)[16],
+                                            uint16_t* h, int64_t ldh, int m0, int c_first, int M,
+                                            int N, int lane, unsigned* err) {
+  const int b = (t.count & 1) * 1024;
+  float* give = reinterpret_cast<float*>(t.mine + b) + lane;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) give[32 * i] = t.is_up ? v[i] : v[8 + i];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(t.bar);
+  if (!mbar_wait_warp(t.bar, static_cast<uint32_t>(t.count & 1), err, kErrWaitEpilogue)) return false;
+  ++t.count;
+  uint8_t* stg = t.mine + (b ^ 1024);
+  if (e.g) stage_and_flush<16>(stg, v, t.is_up ? e.u : e.g, e.ldgu, m0, c_first, M, N, lane);
+  const float* got = reinterpret_cast<const float*>(t.theirs + b) + lane;
+  float o[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = got[32 * i];
+    const float own = t.is_up ? v[8 + i] : v[i];
+    o[i] = t.is_up ? act_value(e.act, x) * own : act_value(e.act, own) * x;
+  }
+  stage_and_flush<8>(stg, o, h, ldh, m0 + (t.is_up ? 8 : 0), c_first, M, N, lane);
+  return true;
+}
+
+template <int BT, int NSUB, bool GROUPED, int EPI>
 __global__ void __launch_bounds__(512, 1)
     w8a16_gemm_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_x,
                       const float* __restrict__ sw, __nv_bfloat16* __restrict__ y, int64_t ldy,
                       int M, int N, int KB, int mtiles, int ntiles_total, int gm, int dp_tiles,
-                      int early_weights, float* __restrict__ part, unsigned* __restrict__ err) {
-  using C = W8A16Cfg<BT, NSUB>;
+                      int early_weights, float* __restrict__ part, unsigned* __restrict__ err,
+                      const __grid_constant__ EpiParams<EPI> ep) {
+  using C = W8A16Cfg<BT, NSUB, EPI>;
+  constexpr bool GATED = EPI == kEpiGated;
+  constexpr int TILE_N = GATED ? 64 : 128;  // output columns of a tile
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
@@ -254,20 +378,21 @@ __global__ void __launch_bounds__(512, 1)
   uint8_t* sX = smem + C::QS * C::Q_BYTES;  // XS x X_BYTES
   uint8_t* sOut = sX + C::XS * C::X_BYTES;  // 4 NSUB x OUT_BYTES output transposition
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::SMEM_TILES);
-  uint64_t* qfull = bars;              // codes landed          (1 arrival + tx)
+  uint64_t* qfull = bars;              // codes landed          (1 arrival + tx; gated 2)
   uint64_t* qempty = qfull + C::QS;    // codes read            (4 expansion warps)
   uint64_t* xfull = qempty + C::QS;    // x sub-tile landed     (1 arrival + tx)
   uint64_t* afull = xfull + C::XS;     // A buffer written      (4 expansion warps)
   uint64_t* done = afull + C::AB;      // item's MMAs complete  (1 commit)
   uint64_t* pempty = done + C::RD;     // partial consumed      (4 or 8 epilogue warps)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pempty + C::PB * 2);
+  uint64_t* trade = pempty + C::PB * 2;  // gate/up trade      (2 warps), one per pair
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(trade + C::XW);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int total_slabs = Schedule(KB, ntiles_total, dp_tiles).slabs();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::QS; ++s) {
-      mbar_init(&qfull[s], 1);
+      mbar_init(&qfull[s], GATED ? 2 : 1);
       mbar_init(&qempty[s], 4);
     }
     for (int s = 0; s < C::XS; ++s) mbar_init(&xfull[s], 1);
@@ -276,6 +401,7 @@ __global__ void __launch_bounds__(512, 1)
     // One barrier per (partial slot, issuer). NSUB == 2: all eight epilogue
     // warps promote every item.
     for (int b = 0; b < C::PB * 2; ++b) mbar_init(&pempty[b], NSUB == 2 ? 8 : 4);
+    for (int b = 0; b < C::XW; ++b) mbar_init(&trade[b], 2);
     mbar_init_fence();
   }
   if (warp == 2) {
@@ -299,9 +425,16 @@ __global__ void __launch_bounds__(512, 1)
   const int wg = warp >> 2;
   if (wg == 0) {
     setmaxnreg_dec<64>();
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && lane < (GATED ? 2 : 1)) {
       // ------------------------------------------------ weight-code producer
-      tma_prefetch_map(&tm_q);
+      // (gated: lane 0 loads the 64 gate rows of a slab, lane 1 the up rows)
+      const CUtensorMap* map = &tm_q;
+      if constexpr (GATED) {
+        if (lane == 1) map = &ep.tm_up;
+      }
+      constexpr uint32_t kBytes = C::Q_BYTES / (GATED ? 2 : 1);
+      const uint32_t part_off = GATED ? lane * kBytes : 0u;
+      tma_prefetch_map(map);
       if (!early_weights) pdl_wait();
       int j = 0;  // slab counter (across tiles)
       bool ok = true;
@@ -310,15 +443,15 @@ __global__ void __launch_bounds__(512, 1)
       while (ok && sc.next(tile, kb0, kb1)) {
         int mt, nt;
         tile_of<GROUPED>(tile, mtiles, ntiles_total, gm, mt, nt);
-        const int n0 = nt * 128;
+        const int n0 = nt * TILE_N;
         for (int kb = kb0; kb < kb1; ++kb, ++j) {
           const int qs = j % C::QS;
           if (!mbar_wait_sleepy(&qempty[qs], ring_parity(j, C::QS) ^ 1u, err, kErrWaitLoad)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(&qfull[qs], C::Q_BYTES);
-          tma_load_2d(sQ + qs * C::Q_BYTES, &tm_q, &qfull[qs], kb * 128, n0);
+          mbar_arrive_expect_tx(&qfull[qs], kBytes);
+          tma_load_2d(sQ + qs * C::Q_BYTES + part_off, map, &qfull[qs], kb * 128, n0);
         }
       }
       // Drain: every load issued has landed before the CTA may exit.
@@ -402,6 +535,10 @@ __global__ void __launch_bounds__(512, 1)
     if constexpr (NSUB == 2) {
       // ------------------------------------ promotion/epilogue (two sub-tiles)
       pdl_wait();  // y may still be read by the kernel before
+      const float* sw_of_quad = sw;
+      if constexpr (GATED) {
+        if ((warp & 3) >= 2) sw_of_quad = ep.e.s_up;
+      }
       // All eight warps promote every item: warp 8 + 4h + q owns TMEM lane
       // quadrant q and token columns [64h, 64h + 64) of each item's partial,
       // so a partial is read by eight warps at once (two 32-column loads
@@ -410,7 +547,9 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + C::TMEM_P +
                               static_cast<uint32_t>(64 * h);
       uint8_t* stg = sOut + ew * C::OUT_BYTES;
-      const int rr = lane >> 1, hh = lane & 1;  // row and half this lane stores
+      GateTrade tr;
+      if constexpr (GATED)
+        tr = {stg, sOut + (ew ^ 2) * C::OUT_BYTES, &trade[2 * h + (quad & 1)], quad >= 2};
       int j = 0;
       bool ok = true;
       bool first_sk = true;  // the next stream-K segment is this CTA's first
@@ -419,8 +558,8 @@ __global__ void __launch_bounds__(512, 1)
       while (ok && sc.next(tile, kb0, kb1)) {
         int mt, nt;
         tile_of<GROUPED>(tile, mtiles, ntiles_total, gm, mt, nt);
-        const int m0 = mt * (BT * NSUB), n0 = nt * 128;
-        const float* sw_row = sw + static_cast<int64_t>(n0 >> 7) * KB;
+        const int m0 = mt * (BT * NSUB), n0 = nt * TILE_N;
+        const float* sw_row = sw_of_quad + static_cast<int64_t>(n0 >> 7) * KB;
         uint64_t acc[64];  // acc[32t + p]: tokens 128t + 64h + 2p and 2p + 1
 #pragma unroll
         for (int e = 0; e < 64; ++e) acc[e] = 0ull;
@@ -476,30 +615,28 @@ __global__ void __launch_bounds__(512, 1)
         }
         // Output: sixteen tokens at a time through shared memory as rows of
         // 32 BF16 (this warp's columns of y), then 32-byte stores per lane.
-        const int nw = n0 + quad * 32;  // first column of this warp
+        const int nw = n0 + (GATED ? (quad & 1) : quad) * 32;  // first column of this warp
+        float bias = 0.0f;
+        if constexpr (EPI == kEpiFused) {
+          if (ep.e.bias && nw + lane < N) bias = bf16_bits_to_f32(__ldg(ep.e.bias + nw + lane));
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
+            float v[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t b2 = cvt_bf16x2_pair(acc[32 * t + 8 * g + e]);
-              *reinterpret_cast<uint16_t*>(stg + (2 * e) * 64 + lane * 2) = static_cast<uint16_t>(b2 & 0xFFFFu);
-              *reinterpret_cast<uint16_t*>(stg + (2 * e + 1) * 64 + lane * 2) = static_cast<uint16_t>(b2 >> 16);
+            for (int e = 0; e < 8; ++e)
+              asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * e]), "=f"(v[2 * e + 1]) : "l"(acc[32 * t + 8 * g + e]));
+            const int mg = m0 + 128 * t + 64 * h + 16 * g;
+            uint16_t* yo = reinterpret_cast<uint16_t*>(y);
+            if constexpr (EPI == kEpiFused) {
+              fused_group(ep.e, bias, v, stg, yo, ldy, mg, nw, M, N, lane);
+            } else if constexpr (GATED) {
+              ok = ok && gated_group(tr, ep.e, v, yo, ldy, mg, nw, M, N, lane, err);
+            } else {
+              stage_and_flush<16>(stg, v, yo, ldy, mg, nw, M, N, lane);
             }
-            __syncwarp();
-            const uint8_t* src = stg + rr * 64 + hh * 32;
-            const int m = m0 + 128 * t + 64 * h + 16 * g + rr, c0 = nw + 16 * hh;
-            if (m < M && c0 < N) {
-              uint16_t* dst = reinterpret_cast<uint16_t*>(y) + static_cast<int64_t>(m) * ldy + c0;
-              if (c0 + 16 <= N) {
-                reinterpret_cast<uint4*>(dst)[0] = reinterpret_cast<const uint4*>(src)[0];
-                reinterpret_cast<uint4*>(dst)[1] = reinterpret_cast<const uint4*>(src)[1];
-              } else {
-                for (int c = 0; c < N - c0; ++c) dst[c] = reinterpret_cast<const uint16_t*>(src)[c];
-              }
-            }
-            __syncwarp();  // the next group overwrites the buffer
           }
         }
       }
@@ -508,6 +645,13 @@ __global__ void __launch_bounds__(512, 1)
       pdl_wait();  // y and the workspace may still be in use by the kernel before
       const int t = (warp - 8) >> 2;  // token sub-tile
       const int quad = warp & 3;
+      const float* sw_of_quad = sw;
+      GateTrade tr;
+      if constexpr (GATED) {
+        if (quad >= 2) sw_of_quad = ep.e.s_up;
+        const int ew = warp - 8;
+        tr = {sOut + ew * C::OUT_BYTES, sOut + (ew ^ 2) * C::OUT_BYTES, &trade[quad & 1], quad >= 2};
+      }
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + C::TMEM_P;
       int j = 0;
       bool ok = true;
@@ -517,8 +661,8 @@ __global__ void __launch_bounds__(512, 1)
       while (ok && sc.next(tile, kb0, kb1)) {
         int tm, tn;
         tile_of<GROUPED>(tile, mtiles, ntiles_total, gm, tm, tn);
-        const int m0 = tm * (BT * NSUB), n0 = tn * 128;
-        const float* sw_row = sw + static_cast<int64_t>(n0 >> 7) * KB;
+        const int m0 = tm * (BT * NSUB), n0 = tn * TILE_N;
+        const float* sw_row = sw_of_quad + static_cast<int64_t>(n0 >> 7) * KB;
         uint64_t acc[BT / 2];
 #pragma unroll
         for (int e = 0; e < BT / 2; ++e) acc[e] = 0ull;
@@ -576,30 +720,26 @@ __global__ void __launch_bounds__(512, 1)
         // through shared memory as rows of 32 BF16, so that each lane then
         // stores 16 contiguous values (32 bytes) of one row of y.
         const int mt = m0 + t * BT;
-        const int nw = n0 + quad * 32;  // first column of this warp
+        const int nw = n0 + (GATED ? (quad & 1) : quad) * 32;  // first column of this warp
         uint8_t* stg = sOut + (warp - 8) * C::OUT_BYTES;
-        const int rr = lane >> 1, hh = lane & 1;  // row and half this lane stores
+        float bias = 0.0f;
+        if constexpr (EPI == kEpiFused) {
+          if (ep.e.bias && nw + lane < N) bias = bf16_bits_to_f32(__ldg(ep.e.bias + nw + lane));
+        }
 #pragma unroll
         for (int g = 0; g < BT / 16; ++g) {
+          float v[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t b2 = cvt_bf16x2_pair(acc[8 * g + e]);
-            *reinterpret_cast<uint16_t*>(stg + (2 * e) * 64 + lane * 2) = static_cast<uint16_t>(b2 & 0xFFFFu);
-            *reinterpret_cast<uint16_t*>(stg + (2 * e + 1) * 64 + lane * 2) = static_cast<uint16_t>(b2 >> 16);
+          for (int e = 0; e < 8; ++e)
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * e]), "=f"(v[2 * e + 1]) : "l"(acc[8 * g + e]));
+          uint16_t* yo = reinterpret_cast<uint16_t*>(y);
+          if constexpr (EPI == kEpiFused) {
+            fused_group(ep.e, bias, v, stg, yo, ldy, mt + 16 * g, nw, M, N, lane);
+          } else if constexpr (GATED) {
+            ok = ok && gated_group(tr, ep.e, v, yo, ldy, mt + 16 * g, nw, M, N, lane, err);
+          } else {
+            stage_and_flush<16>(stg, v, yo, ldy, mt + 16 * g, nw, M, N, lane);
           }
-          __syncwarp();
-          const uint8_t* src = stg + rr * 64 + hh * 32;
-          const int m = mt + 16 * g + rr, c0 = nw + 16 * hh;
-          if (m < M && c0 < N) {
-            uint16_t* dst = reinterpret_cast<uint16_t*>(y) + static_cast<int64_t>(m) * ldy + c0;
-            if (c0 + 16 <= N) {
-              reinterpret_cast<uint4*>(dst)[0] = reinterpret_cast<const uint4*>(src)[0];
-              reinterpret_cast<uint4*>(dst)[1] = reinterpret_cast<const uint4*>(src)[1];
-            } else {
-              for (int c = 0; c < N - c0; ++c) dst[c] = reinterpret_cast<const uint16_t*>(src)[c];
-            }
-          }
-          __syncwarp();  // the next group overwrites the buffer
         }
       }
     } else {
@@ -660,41 +800,71 @@ SplitTiles split_tiles(int64_t ntiles, int64_t KB, int64_t G) {
 // a single CTA were written directly. Launched as a programmatic dependent
 // of the GEMM: it waits for the GEMM grid to complete before it reads a
 // partial.
-template <int TOK>
+// kEpiGated: a tile is 64 outputs, its gate rows 0-63 and up rows 64-127; a
+// thread sums both rows of its output for two of the eight tokens.
+template <int TOK, int EPI>
 __global__ void __launch_bounds__(256) w8a16_streamk_fixup(const __grid_constant__ SplitTiles st,
                                                            const float* __restrict__ part,
                                                            uint16_t* __restrict__ y, int64_t ldy,
-                                                           int M, int N, int mtiles, int gm) {
+                                                           int M, int N, int mtiles, int gm,
+                                                           const __grid_constant__ EpiParams<EPI> ep) {
   pdl_launch_dependents();  // the next linear may be scheduled; it waits for this grid
   pdl_wait();
+  constexpr bool GATED = EPI == kEpiGated;
+  constexpr int TILE_N = GATED ? 64 : 128;
+  constexpr int TSTEP = 256 / TILE_N;       // tokens side by side in a block
+  constexpr int NT = 8 / TSTEP;             // tokens per thread
   const int i = static_cast<int>(blockIdx.x);
-  const int r = threadIdx.x & 127;
+  const int r = threadIdx.x % TILE_N;
   int mt, nt;
-  tile_coords(st.tile[i], mtiles, (N + 127) / 128, gm, mt, nt);
-  const int n = nt * 128 + r;
+  tile_coords(st.tile[i], mtiles, (N + TILE_N - 1) / TILE_N, gm, mt, nt);
+  const int n = nt * TILE_N + r;
   if (n >= N) return;
   const int m0 = mt * TOK;
   const int c0 = st.c0[i], nc = st.ncontrib[i], slot0 = st.slot0[i];
-  const int mbase = static_cast<int>(blockIdx.y) * 8 + (threadIdx.x >> 7);
-  float acc[4];
+  const int mbase = static_cast<int>(blockIdx.y) * 8 + threadIdx.x / TILE_N;
+  float acc[NT], acc_up[NT];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) acc[u] = 0.0f;
+  for (int u = 0; u < NT; ++u) acc[u] = acc_up[u] = 0.0f;
   for (int c = 0; c < nc; ++c) {
     const float* p = part + (static_cast<int64_t>(c0 + c) * 2 + (c == 0 ? slot0 : 0)) * (TOK * 128) + r;
-    float v[4];
+    float v[NT], w[NT];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int m = mbase + 2 * u;
+    for (int u = 0; u < NT; ++u) {
+      const int m = mbase + TSTEP * u;
       v[u] = m < TOK && m0 + m < M ? p[m * 128] : 0.0f;
+      if constexpr (GATED) w[u] = m < TOK && m0 + m < M ? p[m * 128 + 64] : 0.0f;
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) acc[u] += v[u];
+    for (int u = 0; u < NT; ++u) {
+      acc[u] += v[u];
+      if constexpr (GATED) acc_up[u] += w[u];
+    }
+  }
+  float bias = 0.0f;
+  if constexpr (EPI == kEpiFused) {
+    if (ep.e.bias) bias = bf16_bits_to_f32(__ldg(ep.e.bias + n));
   }
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int m = mbase + 2 * u;
-    if (m < TOK && m0 + m < M)
-      y[static_cast<int64_t>(m0 + m) * ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[u]));
+  for (int u = 0; u < NT; ++u) {
+    const int m = mbase + TSTEP * u;
+    if (m < TOK && m0 + m < M) {
+      const int64_t row = m0 + m;
+      float o = acc[u];
+      if constexpr (EPI == kEpiFused) {
+        o += bias;
+        if (ep.e.preact) ep.e.preact[row * ep.e.ldp + n] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+        o = act_value(ep.e.act, o);
+        if (ep.e.residual) o += bf16_bits_to_f32(ep.e.residual[row * ep.e.ldr + n]);
+      } else if constexpr (GATED) {
+        if (ep.e.g) {
+          ep.e.g[row * ep.e.ldgu + n] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+          ep.e.u[row * ep.e.ldgu + n] = __bfloat16_as_ushort(__float2bfloat16_rn(acc_up[u]));
+        }
+        o = act_value(ep.e.act, o) * acc_up[u];
+      }
+      y[row * ldy + n] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
+    }
   }
 }
 
@@ -704,18 +874,24 @@ size_t streamk_bytes(int64_t grid, int tok) {
   return static_cast<size_t>(grid) * 2 * tok * 128 * sizeof(float);
 }
 
-template <int BT, int NSUB, bool GROUPED>
+template <int BT, int NSUB, bool GROUPED, int EPI>
 cudaError_t launch_bt(const Launch& L, const uint16_t* x, int64_t ldx, const uint8_t* q,
                       int64_t ldq, const float* sw, uint16_t* y, int64_t ldy, int64_t M,
-                      int64_t N, int64_t K, void* ws, size_t ws_bytes, bool early_weights) {
-  using C = W8A16Cfg<BT, NSUB>;
+                      int64_t N, int64_t K, void* ws, size_t ws_bytes, bool early_weights,
+                      EpiParams<EPI>& ep) {
+  using C = W8A16Cfg<BT, NSUB, EPI>;
   constexpr int TOK = BT * NSUB;
+  constexpr int TILE_N = EPI == kEpiGated ? 64 : 128;
   CUtensorMap tq, tx;
-  if (!make_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, N, ldq, 128, 128))
+  if (!make_tmap_2d(&tq, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, N, ldq, 128, TILE_N))
     return cudaErrorInvalidValue;
+  if constexpr (EPI == kEpiGated) {
+    if (!make_tmap_2d(&ep.tm_up, CU_TENSOR_MAP_DATA_TYPE_UINT8, ep.e.q_up, K, N, ldq, 128, TILE_N))
+      return cudaErrorInvalidValue;
+  }
   if (!make_tmap_2d(&tx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, K, M, ldx * 2, 64, BT))
     return cudaErrorInvalidValue;
-  auto kern = w8a16_gemm_kernel<BT, NSUB, GROUPED>;
+  auto kern = w8a16_gemm_kernel<BT, NSUB, GROUPED, EPI>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   {
@@ -730,7 +906,7 @@ cudaError_t launch_bt(const Launch& L, const uint16_t* x, int64_t ldx, const uin
     }();
     if (regs != cudaSuccess) return regs;
   }
-  const int64_t mtiles = cdiv(M, TOK), tiles = mtiles * cdiv(N, 128);
+  const int64_t mtiles = cdiv(M, TOK), tiles = mtiles * cdiv(N, TILE_N);
   const int gm = GROUPED ? raster_group(mtiles, TOK * K * 2, kRasterBytesW8A16) : static_cast<int>(mtiles);
   // Slab and item counters are 32-bit per CTA.
   if (tiles * cdiv(K, 128) * NSUB > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
@@ -779,7 +955,7 @@ cudaError_t launch_bt(const Launch& L, const uint16_t* x, int64_t ldx, const uin
                            static_cast<int>(M), static_cast<int>(N), static_cast<int>(KB),
                            static_cast<int>(mtiles), static_cast<int>(tiles), gm,
                            static_cast<int>(dp_tiles), early_weights ? 1 : 0,
-                           static_cast<float*>(ws), L.err);
+                           static_cast<float*>(ws), L.err, ep);
     if (e != cudaSuccess) return e;
   }
   if (dp_tiles == tiles || grid < 2) return cudaSuccess;
@@ -798,15 +974,28 @@ cudaError_t launch_bt(const Launch& L, const uint16_t* x, int64_t ldx, const uin
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, w8a16_streamk_fixup<TOK>, st, static_cast<const float*>(ws), y,
+  return cudaLaunchKernelEx(&cfg, w8a16_streamk_fixup<TOK, EPI>, st, static_cast<const float*>(ws), y,
                             ldy, static_cast<int>(M), static_cast<int>(N), static_cast<int>(mtiles),
-                            gm);
+                            gm, ep);
 }
 
-}  // namespace
-
-namespace {
 int token_tile(int64_t M) { return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)); }
+
+template <int EPI>
+cudaError_t launch_epi(const Launch& L, const uint16_t* x, int64_t ldx, const uint8_t* q,
+                       int64_t ldq, const float* sw, uint16_t* y, int64_t ldy, int64_t M, int64_t N,
+                       int64_t K, void* ws, size_t ws_bytes, bool early_weights,
+                       EpiParams<EPI>& ep) {
+  if (M <= 16) return launch_bt<16, 1, false, EPI>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights, ep);
+  if (M <= 32) return launch_bt<32, 1, false, EPI>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights, ep);
+  if (M <= 64) return launch_bt<64, 1, false, EPI>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights, ep);
+  if (M <= 128) return launch_bt<128, 1, false, EPI>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights, ep);
+  // Activations larger than the raster budget run in raster groups.
+  if (raster_group(cdiv(M, 256), 256 * K * 2, kRasterBytesW8A16) < cdiv(M, 256))
+    return launch_bt<128, 2, true, EPI>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights, ep);
+  return launch_bt<128, 2, false, EPI>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights, ep);
+}
+
 }  // namespace
 
 // M <= 128 runs stream-K: FP32 partials of split tiles, two slots per CTA
@@ -825,14 +1014,24 @@ size_t w8a16_workspace_required(int64_t M, int64_t N, int64_t K) {
 cudaError_t launch_w8a16_gemm(const Launch& L, const uint16_t* x, int64_t ldx, const uint8_t* q,
                               int64_t ldq, const float* sw, uint16_t* y, int64_t ldy, int64_t M,
                               int64_t N, int64_t K, void* ws, size_t ws_bytes, bool early_weights) {
-  if (M <= 16) return launch_bt<16, 1, false>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights);
-  if (M <= 32) return launch_bt<32, 1, false>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights);
-  if (M <= 64) return launch_bt<64, 1, false>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights);
-  if (M <= 128) return launch_bt<128, 1, false>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights);
-  // Activations larger than the raster budget run in raster groups.
-  if (raster_group(cdiv(M, 256), 256 * K * 2, kRasterBytesW8A16) < cdiv(M, 256))
-    return launch_bt<128, 2, true>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights);
-  return launch_bt<128, 2, false>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights);
+  EpiParams<kEpiPlain> ep;
+  return launch_epi<kEpiPlain>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, early_weights, ep);
+}
+
+cudaError_t launch_w8a16_fused(const Launch& L, const uint16_t* x, int64_t ldx, const uint8_t* q,
+                               int64_t ldq, const float* sw, uint16_t* y, int64_t ldy, int64_t M,
+                               int64_t N, int64_t K, void* ws, size_t ws_bytes, const FusedEpi& e) {
+  EpiParams<kEpiFused> ep;
+  ep.e = e;
+  return launch_epi<kEpiFused>(L, x, ldx, q, ldq, sw, y, ldy, M, N, K, ws, ws_bytes, false, ep);
+}
+
+cudaError_t launch_w8a16_gated(const Launch& L, const uint16_t* x, int64_t ldx, const uint8_t* q,
+                               int64_t ldq, const float* sw, uint16_t* h, int64_t ldh, int64_t M,
+                               int64_t N, int64_t K, void* ws, size_t ws_bytes, const GatedEpi& e) {
+  EpiParams<kEpiGated> ep;
+  ep.e = e;
+  return launch_epi<kEpiGated>(L, x, ldx, q, ldq, sw, h, ldh, M, N, K, ws, ws_bytes, false, ep);
 }
 
 }  // namespace fp8blk

@@ -39,10 +39,23 @@
 //              chunks); the last < 8 columns of a ragged N are written from
 //              the staging buffer with plain stores.
 // Every wait is bounded (kWaitLimitCycles) and reports to the error word.
+//
+// EPI chooses what follows the sums (epilogue.cuh). kEpiFused adds the bias,
+// applies the activation, adds the residual and rounds once; a thread holds
+// one token row, so it reads its row of the residual in 16-byte pieces, all
+// of a 64-column half before the first is used, and the bias as a broadcast.
+// kEpiGated runs two weights as one: a tile's 256 weight rows are 128 gate
+// rows and the 128 up rows of the same outputs (two 128-row boxes per slab, one
+// issued by each of two lanes of warp 1), and an epilogue warp takes 64 gate
+// columns and the same 64 up columns of the partial, so g and u of an output
+// meet in one thread and act(g) * u is stored from the staging buffer as a
+// plain y is: the pre-activations never leave the SM unless the caller keeps
+// them. The multiply work per slab is unchanged.
 #include <cuda_bf16.h>
 
 #include <cstring>
 
+#include "epilogue.cuh"
 #include "internal.cuh"
 #include "ptx.cuh"
 
@@ -85,19 +98,60 @@ __device__ __forceinline__ bool wait_use(uint64_t* bar, int use, unsigned* err, 
   return mbar_wait(bar, static_cast<uint32_t>(use & 1), err, flag);
 }
 
+// 64 columns of one row per lane, from 32 column pairs, into the swizzled
+// staging buffer: 16-byte chunk c of row r sits at chunk position c ^ (r % 8).
+__device__ __forceinline__ void stage_row(uint8_t* srow, int lane, const uint64_t* v) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint4 o;
+    o.x = cvt_bf16x2_pair(v[4 * c + 0]);
+    o.y = cvt_bf16x2_pair(v[4 * c + 1]);
+    o.z = cvt_bf16x2_pair(v[4 * c + 2]);
+    o.w = cvt_bf16x2_pair(v[4 * c + 3]);
+    *reinterpret_cast<uint4*>(srow + ((c ^ (lane & 7)) << 4)) = o;
+  }
+}
+
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+// Stores the staged 32 x 64 block at (row r0, column base): by TMA up to
+// column n_tma, the last < 8 columns of a ragged N by plain stores.
+__device__ __forceinline__ void store_staged(const CUtensorMap* map, const uint8_t* stage,
+                                             const uint8_t* srow, uint16_t* dst_row, int lane,
+                                             int base, int r0, int m, int M, int N, int n_tma) {
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0 && r0 < M && base < n_tma) {
+    tma_store_2d(map, stage, base, r0);
+    tma_store_commit();
+  }
+  if (n_tma < N && n_tma >= base && n_tma < base + 64 && m < M) {
+    const int cl = n_tma - base;  // first tail column within these 64
+    const uint16_t* src =
+        reinterpret_cast<const uint16_t*>(srow + (((cl >> 3) ^ (lane & 7)) << 4));
+    for (int e = 0; e < N - n_tma; ++e) dst_row[n_tma + e] = src[e];
+  }
+}
+
+template <int EPI>
 __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
     w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_y, const float* __restrict__ sx,
                      int64_t ldsx, const float* __restrict__ sw, uint16_t* __restrict__ y,
                      int64_t ldy, int M, int N, int n_tma, int KB, int mtiles, int ntiles_total,
-                     int gm, int a_bytes, unsigned* __restrict__ err) {
+                     int gm, int a_bytes, unsigned* __restrict__ err,
+                     const __grid_constant__ EpiParams<EPI> ep) {
   using C = W8A8Cfg;
+  constexpr bool GATED = EPI == kEpiGated;
+  constexpr int TILE_N = GATED ? C::BN / 2 : C::BN;  // output columns of a tile
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;                            // ST stages: A then B
   uint8_t* sOut = smem + C::ST * C::STAGE_BYTES;             // EPI_WARPS x 4 KB staging
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::SMEM_TILES);
-  uint64_t* full = bars;               // stage landed       (2 producers + tx)
+  uint64_t* full = bars;               // stage landed       (2 or 3 producers + tx)
   uint64_t* done = full + C::ST;       // slab's MMAs done   (1 commit)
   uint64_t* pempty = done + C::RD;     // partial consumed   (8 epilogue warps), one per issuer
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pempty + 2);
@@ -109,7 +163,7 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
   const int total_slabs = my_tiles * KB;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::ST; ++s) mbar_init(&full[s], 2);
+    for (int s = 0; s < C::ST; ++s) mbar_init(&full[s], GATED ? 3 : 2);
     for (int b = 0; b < C::RD; ++b) mbar_init(&done[b], 1);
     for (int b = 0; b < 2; ++b) mbar_init(&pempty[b], C::EPI_WARPS);
     mbar_init_fence();
@@ -129,12 +183,21 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
   // Each warpgroup sets its register budget at the top of its role.
   if (warp < 4) {
     setmaxnreg_dec<C::REG_CTRL>();
-    if (warp < 2 && lane == 0) {
+    if (warp < 2 && (lane == 0 || (GATED && warp == 1 && lane == 1))) {
       // ------------------------------------------------- producers (A, B)
       const bool is_a = warp == 0;
       const CUtensorMap* map = is_a ? &tm_a : &tm_b;
-      const uint32_t bytes = is_a ? static_cast<uint32_t>(a_bytes) : C::B_BYTES;
+      uint32_t bytes = is_a ? static_cast<uint32_t>(a_bytes) : C::B_BYTES;
       uint8_t* dst0 = smem + (is_a ? 0 : C::A_BYTES);
+      if constexpr (GATED) {  // gate rows, then up rows
+        if (!is_a) {
+          bytes = C::B_BYTES / 2;
+          if (lane == 1) {
+            map = &ep.tm_up;
+            dst0 += C::B_BYTES / 2;
+          }
+        }
+      }
       tma_prefetch_map(map);
       // Launched as a programmatic dependent of the activation quantizer:
       // the weights may stream at once, the activation codes only once that
@@ -145,7 +208,7 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
       for (int tile = blockIdx.x; tile < ntiles_total && ok; tile += gridDim.x) {
         int mt, nt;
         tile_coords(tile, mtiles, ntiles_n, gm, mt, nt);
-        const int row0 = is_a ? mt * C::BM : nt * C::BN;
+        const int row0 = is_a ? mt * C::BM : nt * TILE_N;
         for (int kb = 0; kb < KB; ++kb, ++j) {
           const int stage = j & (C::ST - 1);
           if (j >= C::ST) {  // the slab that last used this stage has finished
@@ -192,10 +255,10 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
     pdl_wait();  // the activation scales come from the kernel before
     const int ew = warp - 4;
     const int quad = warp & 3;  // TMEM lanes this warp may access
-    const int h = ew >> 2;      // partial columns [128h, 128h + 128)
+    const int h = ew >> 2;      // partial columns [128h, 128h + 128); gated: 64h.. of each half
     const int row = quad * 32 + lane;
-    const uint32_t t_lane =
-        tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(h * 128);
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) +
+                            static_cast<uint32_t>(h * (TILE_N / 2));
     uint8_t* stage = sOut + ew * C::OUT_BYTES;
     uint8_t* srow = stage + lane * 128;
     int j = 0;
@@ -204,65 +267,137 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
       int mt, nt;
       tile_coords(tile, mtiles, ntiles_n, gm, mt, nt);
       const int m0 = mt * C::BM;
-      const int col0 = nt * C::BN + 128 * h;  // first output column of this warp
+      const int col0 = nt * TILE_N + (TILE_N / 2) * h;  // first output column of this warp
       const bool has_cols = col0 < N;
       const int m = m0 + row;
       // sx is group-major with ldsx covering whole 128-row tiles, so rows
       // past M read padding (their results are never stored).
       const float* sx_col = sx + (m < M ? m : 0);
       const float* sw_row = sw + static_cast<int64_t>(has_cols ? (col0 >> 7) : 0) * KB;
-      uint64_t acc[64];  // column pairs
+      const float* sw_up = nullptr;
+      if constexpr (GATED) sw_up = ep.e.s_up + static_cast<int64_t>(has_cols ? (col0 >> 7) : 0) * KB;
+      uint64_t acc[64];  // column pairs (gated: 32 of the gate, then 32 of up)
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
       // The two scale factors of a slab are loaded one slab ahead and only
       // multiplied when used, so the product does not wait on the loads.
       float fx = has_cols ? __ldg(sx_col) : 0.0f, fw = has_cols ? __ldg(sw_row) : 0.0f;
+      float fu = GATED && has_cols ? __ldg(sw_up) : 0.0f;
       for (int kb = 0; kb < KB; ++kb, ++j) {
         const float c = fx * fw;
-        if (has_cols && kb + 1 < KB) { fx = __ldg(sx_col + (kb + 1) * ldsx); fw = __ldg(sw_row + kb + 1); }
+        const float cu = GATED ? fx * fu : 0.0f;
+        if (has_cols && kb + 1 < KB) {
+          fx = __ldg(sx_col + (kb + 1) * ldsx);
+          fw = __ldg(sw_row + kb + 1);
+          if constexpr (GATED) fu = __ldg(sw_up + kb + 1);
+        }
         if (!mbar_wait_warp(&done[j & (C::RD - 1)], static_cast<uint32_t>((j / C::RD) & 1), err,
                             kErrWaitEpilogue)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        tmem_axpy2<4>(t_lane + static_cast<uint32_t>((j & 1) * C::BN), c, acc);
+        const uint32_t tp = t_lane + static_cast<uint32_t>((j & 1) * C::BN);
+        if constexpr (GATED) {
+          tmem_axpy2<2>(tp, c, acc);
+          tmem_axpy2<2>(tp + 128u, cu, acc + 32);
+        } else {
+          tmem_axpy2<4>(tp, c, acc);
+        }
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pempty[j & 1]);
       }
       if (!ok) break;
       // Output, 64 columns at a time: the staging buffer's previous store has
-      // been read out; 16-byte chunk c of row r sits at chunk position
-      // c ^ (r % 8) (the 128-byte swizzle the store expects).
+      // been read out before it is written again.
       const int r0 = m0 + quad * 32;
+      uint16_t* yrow = y + static_cast<int64_t>(m) * ldy;
+      if constexpr (GATED) {
+        if (ep.e.g) {  // kept pre-activations
+          if (lane == 0) tma_store_wait_read<0>();
+          __syncwarp();
+          stage_row(srow, lane, acc);
+          store_staged(&ep.tm_g, stage, srow, ep.e.g + static_cast<int64_t>(m) * ep.e.ldgu, lane,
+                       col0, r0, m, M, N, n_tma);
+          if (lane == 0) tma_store_wait_read<0>();
+          __syncwarp();
+          stage_row(srow, lane, acc + 32);
+          store_staged(&ep.tm_u, stage, srow, ep.e.u + static_cast<int64_t>(m) * ep.e.ldgu, lane,
+                       col0, r0, m, M, N, n_tma);
+        }
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int base = col0 + 64 * hh;
+        for (int p = 0; p < 32; ++p) {
+          float g0, g1, u0, u1;
+          unpack2(acc[p], g0, g1);
+          unpack2(acc[32 + p], u0, u1);
+          acc[p] = pack_f32x2(act_value(ep.e.act, g0) * u0, act_value(ep.e.act, g1) * u1);
+        }
         if (lane == 0) tma_store_wait_read<0>();
         __syncwarp();
+        stage_row(srow, lane, acc);
+        store_staged(&tm_y, stage, srow, yrow, lane, col0, r0, m, M, N, n_tma);
+      } else {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int p = 32 * hh + 4 * c;
-          uint4 o;
-          o.x = cvt_bf16x2_pair(acc[p + 0]);
-          o.y = cvt_bf16x2_pair(acc[p + 1]);
-          o.z = cvt_bf16x2_pair(acc[p + 2]);
-          o.w = cvt_bf16x2_pair(acc[p + 3]);
-          *reinterpret_cast<uint4*>(srow + ((c ^ (lane & 7)) << 4)) = o;
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && r0 < M && base < n_tma) {
-          tma_store_2d(&tm_y, stage, base, r0);
-          tma_store_commit();
-        }
-        if (n_tma < N && n_tma >= base && n_tma < base + 64 && m < M) {
-          const int cl = n_tma - base;  // first tail column within these 64
-          const uint16_t* src =
-              reinterpret_cast<const uint16_t*>(srow + (((cl >> 3) ^ (lane & 7)) << 4));
-          uint16_t* dst = y + static_cast<int64_t>(m) * ldy + n_tma;
-          for (int e = 0; e < N - n_tma; ++e) dst[e] = src[e];
+        for (int hh = 0; hh < 2; ++hh) {
+          const int base = col0 + 64 * hh;
+          uint64_t* v = acc + 32 * hh;
+          if constexpr (EPI == kEpiFused) {
+            const FusedEpi& e = ep.e;
+            uint4 r[8];
+            if (e.residual && m < M) {
+              const uint16_t* rr = e.residual + static_cast<int64_t>(m) * e.ldr + base;
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                r[c] = make_uint4(0u, 0u, 0u, 0u);
+                if (base + 8 * c + 8 <= N) {
+                  r[c] = *reinterpret_cast<const uint4*>(rr + 8 * c);
+                } else if (base + 8 * c < N) {
+                  uint16_t t8[8];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) t8[i] = base + 8 * c + i < N ? rr[8 * c + i] : uint16_t{0};
+                  r[c] = make_uint4(t8[0] | (t8[1] << 16), t8[2] | (t8[3] << 16),
+                                    t8[4] | (t8[5] << 16), t8[6] | (t8[7] << 16));
+                }
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) r[c] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (e.bias) {
+#pragma unroll
+              for (int p = 0; p < 32; ++p) {
+                const int n = base + 2 * p;
+                float lo, hi;
+                unpack2(v[p], lo, hi);
+                lo += n < N ? bf16_bits_to_f32(__ldg(e.bias + n)) : 0.0f;
+                hi += n + 1 < N ? bf16_bits_to_f32(__ldg(e.bias + n + 1)) : 0.0f;
+                v[p] = pack_f32x2(lo, hi);
+              }
+            }
+            if (e.preact) {
+              if (lane == 0) tma_store_wait_read<0>();
+              __syncwarp();
+              stage_row(srow, lane, v);
+              store_staged(&ep.tm_pre, stage, srow, e.preact + static_cast<int64_t>(m) * e.ldp,
+                           lane, base, r0, m, M, N, n_tma);
+            }
+#pragma unroll
+            for (int p = 0; p < 32; ++p) {
+              const uint32_t rw = p % 4 == 0   ? r[p / 4].x
+                                  : p % 4 == 1 ? r[p / 4].y
+                                  : p % 4 == 2 ? r[p / 4].z
+                                               : r[p / 4].w;
+              float lo, hi;
+              unpack2(v[p], lo, hi);
+              v[p] = pack_f32x2(act_value(e.act, lo) + bf16_lo_to_f32(rw),
+                                act_value(e.act, hi) + bf16_hi_to_f32(rw));
+            }
+          }
+          if (lane == 0) tma_store_wait_read<0>();
+          __syncwarp();
+          stage_row(srow, lane, v);
+          store_staged(&tm_y, stage, srow, yrow, lane, base, r0, m, M, N, n_tma);
         }
       }
     }
@@ -278,12 +413,19 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
   }
 }
 
-}  // namespace
+// A store map over the columns [0, N rounded down to 8) of a BF16 matrix
+// (none if N < 8).
+bool store_map(CUtensorMap* map, const uint16_t* p, int64_t n_tma, int64_t M, int64_t ld) {
+  if (n_tma > 0 && p) return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, n_tma, M, 2 * ld, 64, 32);
+  memset(map, 0, sizeof(*map));
+  return true;
+}
 
-cudaError_t launch_w8a8_gemm(const Launch& L, const uint8_t* qx, int64_t ldqx, const float* sx,
-                             int64_t ldsx, const uint8_t* q, int64_t ldq, const float* sw,
-                             uint16_t* y, int64_t ldy, int64_t M, int64_t N, int64_t K,
-                             bool after_act_quant) {
+template <int EPI>
+cudaError_t launch_epi(const Launch& L, const uint8_t* qx, int64_t ldqx, const float* sx,
+                       int64_t ldsx, const uint8_t* q, int64_t ldq, const float* sw, uint16_t* y,
+                       int64_t ldy, int64_t M, int64_t N, int64_t K, bool after_act_quant,
+                       EpiParams<EPI>& ep) {
   using C = W8A8Cfg;
   CUtensorMap ta, tb, ty;
   // Fewer than BM tokens: load only the first round_up(M, 8) activation rows
@@ -293,17 +435,20 @@ cudaError_t launch_w8a8_gemm(const Launch& L, const uint8_t* qx, int64_t ldqx, c
   if (!make_tmap_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_UINT8, qx, K, M, ldqx, 128,
                     static_cast<uint32_t>(a_rows)))
     return cudaErrorInvalidValue;
-  if (!make_tmap_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, N, ldq, 128, C::BN))
+  constexpr int kTileN = EPI == kEpiGated ? C::BN / 2 : C::BN;
+  if (!make_tmap_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, N, ldq, 128, kTileN))
     return cudaErrorInvalidValue;
-  // The output map covers columns [0, N rounded down to 8); none if N < 8.
   const int64_t n_tma = N & ~int64_t{7};
-  if (n_tma > 0) {
-    if (!make_tmap_2d(&ty, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, y, n_tma, M, 2 * ldy, 64, 32))
+  if (!store_map(&ty, y, n_tma, M, ldy)) return cudaErrorInvalidValue;
+  if constexpr (EPI == kEpiFused) {
+    if (!store_map(&ep.tm_pre, ep.e.preact, n_tma, M, ep.e.ldp)) return cudaErrorInvalidValue;
+  } else if constexpr (EPI == kEpiGated) {
+    if (!make_tmap_2d(&ep.tm_up, CU_TENSOR_MAP_DATA_TYPE_UINT8, ep.e.q_up, K, N, ldq, 128, kTileN) ||
+        !store_map(&ep.tm_g, ep.e.g, n_tma, M, ep.e.ldgu) ||
+        !store_map(&ep.tm_u, ep.e.u, n_tma, M, ep.e.ldgu))
       return cudaErrorInvalidValue;
-  } else {
-    memset(&ty, 0, sizeof(ty));
   }
-  auto kern = w8a8_gemm_kernel;
+  auto kern = w8a8_gemm_kernel<EPI>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   {
@@ -317,7 +462,7 @@ cudaError_t launch_w8a8_gemm(const Launch& L, const uint8_t* qx, int64_t ldqx, c
     }();
     if (regs != cudaSuccess) return regs;
   }
-  const int64_t mtiles = cdiv(M, C::BM), tiles = mtiles * cdiv(N, C::BN);
+  const int64_t mtiles = cdiv(M, C::BM), tiles = mtiles * cdiv(N, kTileN);
   // Slab counters are 32-bit per CTA.
   if (tiles * cdiv(K, 128) > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   const int grid = static_cast<int>(tiles < L.num_sms ? tiles : L.num_sms);
@@ -337,7 +482,35 @@ cudaError_t launch_w8a8_gemm(const Launch& L, const uint8_t* qx, int64_t ldqx, c
                             static_cast<int>(N), static_cast<int>(n_tma),
                             static_cast<int>(cdiv(K, 128)), static_cast<int>(mtiles),
                             static_cast<int>(tiles), raster_group(mtiles, C::BM * K, kRasterBytesW8A8),
-                            static_cast<int>(a_rows * 128), L.err);
+                            static_cast<int>(a_rows * 128), L.err, ep);
+}
+
+}  // namespace
+
+cudaError_t launch_w8a8_gemm(const Launch& L, const uint8_t* qx, int64_t ldqx, const float* sx,
+                             int64_t ldsx, const uint8_t* q, int64_t ldq, const float* sw,
+                             uint16_t* y, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                             bool after_act_quant) {
+  EpiParams<kEpiPlain> ep;
+  return launch_epi<kEpiPlain>(L, qx, ldqx, sx, ldsx, q, ldq, sw, y, ldy, M, N, K, after_act_quant, ep);
+}
+
+cudaError_t launch_w8a8_fused(const Launch& L, const uint8_t* qx, int64_t ldqx, const float* sx,
+                              int64_t ldsx, const uint8_t* q, int64_t ldq, const float* sw,
+                              uint16_t* y, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                              const FusedEpi& e) {
+  EpiParams<kEpiFused> ep;
+  ep.e = e;
+  return launch_epi<kEpiFused>(L, qx, ldqx, sx, ldsx, q, ldq, sw, y, ldy, M, N, K, true, ep);
+}
+
+cudaError_t launch_w8a8_gated(const Launch& L, const uint8_t* qx, int64_t ldqx, const float* sx,
+                              int64_t ldsx, const uint8_t* q, int64_t ldq, const float* sw,
+                              uint16_t* h, int64_t ldh, int64_t M, int64_t N, int64_t K,
+                              const GatedEpi& e) {
+  EpiParams<kEpiGated> ep;
+  ep.e = e;
+  return launch_epi<kEpiGated>(L, qx, ldqx, sx, ldsx, q, ldq, sw, h, ldh, M, N, K, true, ep);
 }
 
 }  // namespace fp8blk

@@ -64,6 +64,28 @@ cudaError_t launch_w8a16_gemm(const Launch& L, const uint16_t* x, int64_t ldx, c
                               int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
                               bool early_weights = false);
 
+// The same GEMMs with an epilogue (epilogue.cuh): W8A8 always right after
+// launch_quantize_act; W8A16 with the workspace rules of launch_w8a16_gemm
+// (gated: those of 2 N outputs).
+struct FusedEpi;
+struct GatedEpi;
+cudaError_t launch_w8a8_fused(const Launch& L, const uint8_t* qx, int64_t ldqx, const float* sx,
+                              int64_t ldsx, const uint8_t* q, int64_t ldq, const float* scale_inv,
+                              uint16_t* y, int64_t ldy, int64_t M, int64_t N, int64_t K,
+                              const FusedEpi& e);
+cudaError_t launch_w8a8_gated(const Launch& L, const uint8_t* qx, int64_t ldqx, const float* sx,
+                              int64_t ldsx, const uint8_t* q, int64_t ldq, const float* scale_inv,
+                              uint16_t* h, int64_t ldh, int64_t M, int64_t N, int64_t K,
+                              const GatedEpi& e);
+cudaError_t launch_w8a16_fused(const Launch& L, const uint16_t* x, int64_t ldx, const uint8_t* q,
+                               int64_t ldq, const float* scale_inv, uint16_t* y, int64_t ldy,
+                               int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
+                               const FusedEpi& e);
+cudaError_t launch_w8a16_gated(const Launch& L, const uint16_t* x, int64_t ldx, const uint8_t* q,
+                               int64_t ldq, const float* scale_inv, uint16_t* h, int64_t ldh,
+                               int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes,
+                               const GatedEpi& e);
+
 // 2-D tiled tensor map (128-byte swizzling unless stated) over a row-major
 // matrix [outer][inner] whose rows are row_bytes apart; out-of-bounds reads
 // are zero-filled and out-of-bounds parts of a store are dropped. Returns
@@ -78,6 +100,18 @@ cudaError_t ensure_smem_limit(const void* kernel, size_t bytes);
 // The workspace a linear call cannot run without (for W8A16 above 128 tokens
 // 0: its stream-K tail runs only when the workspace given is large enough).
 size_t required_workspace(int mode, int64_t M, int64_t N, int64_t K);
+
+// Where the W8A8 calls keep the quantized activations in their workspace:
+// codes [M][ldqx] at offset 0, scales [ceil(K/128)][ldsx] at sx_offset.
+inline int64_t w8a8_ldqx(int64_t K) { return round_up(K, 16); }
+inline int64_t w8a8_ldsx(int64_t M) { return round_up(M, 128); }
+inline int64_t w8a8_sx_offset(int64_t M, int64_t K) { return round_up(M * w8a8_ldqx(K), 256); }
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline fp8blk_status cuda_status(cudaError_t e) {
+  return e == cudaSuccess ? FP8BLK_OK : FP8BLK_ERR_CUDA;
+}
+constexpr int64_t kInt32Max = 0x7FFFFFFFLL;
 
 // The launch context of the current device (checks compute capability 10.x).
 fp8blk_status current_launch(fp8blk_stream stream, Launch* L);

@@ -300,6 +300,162 @@ FP8BLK_EXPORT fp8blk_status fp8blk_streamed_linears(const fp8blk_linear_job* job
                                                     fp8blk_stream compute, fp8blk_stream copy,
                                                     fp8blk_event* events);
 
+/* ---------------------------------------------------------------------------
+ * The feed-forward operators: what a layer does around its linears, in the
+ * kernels of the linears. Weights are in the block-FP8 form of this header;
+ * the backward calls return gradients with respect to the activations and the
+ * dequantized weights (E4M3 code times scale). Activation functions:
+ *   NONE       z
+ *   RELU       max(z, 0)                    (derivative 0 at z = 0)
+ *   GELU       z Phi(z), Phi the normal distribution function
+ *   GELU_TANH  z / 2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))
+ *   SILU       z / (1 + exp(-z))
+ * All of them are computed in FP32 from FP32 sums; BF16 results are rounded
+ * once, to nearest even.
+ * ------------------------------------------------------------------------- */
+typedef enum fp8blk_activation {
+  FP8BLK_ACT_NONE = 0,
+  FP8BLK_ACT_RELU = 1,
+  FP8BLK_ACT_GELU = 2,
+  FP8BLK_ACT_GELU_TANH = 3,
+  FP8BLK_ACT_SILU = 4
+} fp8blk_activation;
+
+/* What follows a linear's product: z = x . dequant(W)^T + bias,
+ * y = act(z) + residual. Null pointers leave a part out. */
+typedef struct fp8blk_epilogue {
+  const void* bias;       /* BF16 [N] or NULL; 2-byte aligned */
+  int32_t activation;     /* an fp8blk_activation */
+  const void* residual;   /* BF16 [M][ldr] or NULL; ldr >= N, ldr % 8 == 0; may be y
+                             itself (same pointer, ldr == ldy), must not overlap it otherwise */
+  int64_t ldr;
+  void* preact;           /* BF16 [M][ldp] or NULL: receives z, rounded to BF16, for the
+                             backward pass; ldp >= N, ldp % 8 == 0 */
+  int64_t ldp;
+} fp8blk_epilogue;
+
+/* ---------------------------------------------------------------------------
+ * fp8blk_linear_w8a16 / fp8blk_linear_w8a8 with an epilogue. Arguments,
+ * workspace and ordering as for those calls; K = 0 gives y = act(bias) +
+ * residual. The FP32 sum is never rounded before the epilogue.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, WORKSPACE, CUDA.
+ * ------------------------------------------------------------------------- */
+FP8BLK_EXPORT fp8blk_status fp8blk_linear_w8a16_epilogue(
+    const void* x, int64_t ldx, const uint8_t* q, int64_t ldq, const float* scale_inv, void* y,
+    int64_t ldy, int64_t M, int64_t N, int64_t K, const fp8blk_epilogue* epilogue, void* workspace,
+    size_t workspace_bytes, fp8blk_stream stream);
+FP8BLK_EXPORT fp8blk_status fp8blk_linear_w8a8_epilogue(
+    const void* x, int64_t ldx, const uint8_t* q, int64_t ldq, const float* scale_inv, void* y,
+    int64_t ldy, int64_t M, int64_t N, int64_t K, const fp8blk_epilogue* epilogue, void* workspace,
+    size_t workspace_bytes, fp8blk_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Gated linear, the first half of a gated feed-forward block: both
+ * projections, the activation and the product in one kernel,
+ *   g = x . dequant(Wg)^T, u = x . dequant(Wu)^T, h[m][n] = BF16(act(g) * u),
+ * with BF16 activations (w8a16) or activations quantized per 1 x 128 K-group
+ * (w8a8), as in the linear calls.
+ *   q_gate, q_up : uint8 [N][ldq], one ldq for both; ldq >= K, ldq % 16 == 0
+ *   s_gate, s_up : float [ceil(N/128)][ceil(K/128)]
+ *                  (a fused [2N][K] weight with N % 128 == 0 is passed as its
+ *                  two halves)
+ *   h    : BF16 [M][ldh], ldh >= N, ldh % 8 == 0                     (output)
+ *   g, u : BF16 [M][ldgu] or both NULL: the pre-activations, rounded to BF16,
+ *          for fp8blk_gated_backward (h itself is computed from the unrounded
+ *          sums); ldgu >= N, ldgu % 8 == 0                            (output)
+ *   workspace : as for the linear calls, for 2 N outputs: fp8blk_workspace_size(
+ *          mode, M, 2 * N, K) bytes, required and optional as there.
+ * Outputs must not overlap the inputs or one another.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, WORKSPACE, CUDA.
+ * ------------------------------------------------------------------------- */
+FP8BLK_EXPORT fp8blk_status fp8blk_gated_linear_w8a16(
+    const void* x, int64_t ldx, const uint8_t* q_gate, const float* s_gate, const uint8_t* q_up,
+    const float* s_up, int64_t ldq, int32_t activation, void* h, int64_t ldh, void* g, void* u,
+    int64_t ldgu, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+    fp8blk_stream stream);
+FP8BLK_EXPORT fp8blk_status fp8blk_gated_linear_w8a8(
+    const void* x, int64_t ldx, const uint8_t* q_gate, const float* s_gate, const uint8_t* q_up,
+    const float* s_up, int64_t ldq, int32_t activation, void* h, int64_t ldh, void* g, void* u,
+    int64_t ldgu, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+    fp8blk_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Backward pass of the gated product: from dh and the kept g, u,
+ *   dg = BF16(dh * u * act'(g)),  du = BF16(dh * act(g)).
+ *   dh   : BF16 [M][lddh]; g, u : BF16 [M][ldgu]                     (input)
+ *   dgu  : BF16 [M][lddgu], lddgu >= 2 * round_up(N, 128): dg in columns
+ *          [0, N), du in [Np, Np + N) with Np = round_up(N, 128); columns
+ *          [N, Np) and [Np + N, 2 Np) are set to 0                    (output)
+ * All leading dimensions % 8 == 0. That layout is the activation operand of
+ * the linears against the two transposed weights side by side (see
+ * fp8blk_transpose_weight): dx = dg . Wg + du . Wu in one product. Must not
+ * overlap. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
+ * ------------------------------------------------------------------------- */
+FP8BLK_EXPORT fp8blk_status fp8blk_gated_backward(const void* dh, int64_t lddh, const void* g,
+                                                  const void* u, int64_t ldgu, int32_t activation,
+                                                  void* dgu, int64_t lddgu, int64_t M, int64_t N,
+                                                  fp8blk_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Backward pass of an epilogue: from dy and the kept z,
+ *   dz = BF16(dy * act'(z)),  dbias[n] = sum_m dy[m][n] * act'(z[m][n])
+ * (the residual's gradient is dy itself). dbias is summed in FP32 from the
+ * unrounded products, in an order that depends on M and N alone.
+ *   dy : BF16 [M][lddy]; z : BF16 [M][ldz], may be NULL with NONE    (input)
+ *   dz    : BF16 [M][lddz] or NULL; may be dy or z itself             (output)
+ *   dbias : float [N] or NULL, 4-byte aligned                         (output)
+ *   workspace : fp8blk_epilogue_backward_workspace_size(M, N) bytes, 256-byte
+ *           aligned, needed when dbias is given (its contents are scratch)
+ * All leading dimensions % 8 == 0. M = 0 sets dbias to 0.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, WORKSPACE, CUDA.
+ * ------------------------------------------------------------------------- */
+FP8BLK_EXPORT fp8blk_status fp8blk_epilogue_backward(const void* dy, int64_t lddy, const void* z,
+                                                     int64_t ldz, int32_t activation, void* dz,
+                                                     int64_t lddz, float* dbias, int64_t M,
+                                                     int64_t N, void* workspace,
+                                                     size_t workspace_bytes, fp8blk_stream stream);
+
+/* Workspace bytes of fp8blk_epilogue_backward with dbias. Pure host function;
+ * 0 for negative sizes, and where no workspace is needed. */
+FP8BLK_EXPORT size_t fp8blk_epilogue_backward_workspace_size(int64_t M, int64_t N);
+
+/* ---------------------------------------------------------------------------
+ * Transposed weight: qt[k][n] = q[n][k], st[k/128][n/128] = s[n/128][k/128].
+ * The blocks are square, so the transpose of a block-FP8 weight is one, code
+ * for code, and dx = dz . dequant(W) is a linear call on (qt, st):
+ * fp8blk_linear_w8a16(dz, qt, st) with N and K exchanged.
+ *   q  : uint8 [N][ldq], ldq >= K, ldq % 16 == 0; scale_inv as above (input)
+ *   qt : uint8 [K][ldqt], ldqt >= round_up(N, 128) if zero_pad, else N;
+ *        ldqt % 16 == 0; columns [N, round_up(N, 128)) are set to 0 if
+ *        zero_pad, else not written                                   (output)
+ *   st : float [ceil(K/128)][ldst], ldst >= ceil(N/128)               (output)
+ * Two weights go side by side for a gated block: gate into columns [0, N) and
+ * up into [Np, Np + N) of one qt with ldqt = 2 Np (Np = round_up(N, 128)),
+ * both with zero_pad, and their scales into one st with ldst = 2 Np / 128.
+ * Must not overlap. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
+ * ------------------------------------------------------------------------- */
+FP8BLK_EXPORT fp8blk_status fp8blk_transpose_weight(const uint8_t* q, int64_t ldq,
+                                                    const float* scale_inv, int64_t N, int64_t K,
+                                                    uint8_t* qt, int64_t ldqt, float* st,
+                                                    int64_t ldst, int32_t zero_pad,
+                                                    fp8blk_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Weight gradient of a linear: dw[n][k] = sum_m dz[m][n] * x[m][k], BF16
+ * operands, FP32 sums in token order of whole 64-token steps.
+ *   dz : BF16 [M][lddz], lddz >= N; x : BF16 [M][ldx], ldx >= K      (input)
+ *   dw : float (dw_fp32 = 1) or BF16 (dw_fp32 = 0) [N][lddw], lddw >= K (output)
+ *   accumulate : 1 adds the sums to dw (FP32 only), 0 overwrites it
+ * lddz, ldx % 8 == 0; lddw % 4 == 0 (FP32) or % 8 == 0 (BF16). M = 0 sets dw
+ * to 0, or leaves it with accumulate. No workspace.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
+ * ------------------------------------------------------------------------- */
+FP8BLK_EXPORT fp8blk_status fp8blk_linear_grad_weight(const void* dz, int64_t lddz, const void* x,
+                                                      int64_t ldx, void* dw, int64_t lddw,
+                                                      int32_t dw_fp32, int32_t accumulate,
+                                                      int64_t M, int64_t N, int64_t K,
+                                                      fp8blk_stream stream);
+
 /* Workspace bytes for a linear: mode 0 = W8A16, 1 = W8A8. Pure host function;
  * returns 0 for an invalid mode or negative sizes. */
 FP8BLK_EXPORT size_t fp8blk_workspace_size(int mode, int64_t M, int64_t N, int64_t K);
