@@ -42,7 +42,7 @@ fp8blk_status linear_epilogue(int mode, const void* x, int64_t ldx, const uint8_
                                      required_workspace(mode, M, N, K));
   if (st != FP8BLK_OK) return st;
   if (M == 0 || N == 0) return FP8BLK_OK;
-  if (!aligned(ep->bias, 2)) return FP8BLK_ERR_ALIGNMENT;
+  if (!aligned(ep->bias, 16)) return FP8BLK_ERR_ALIGNMENT;
   if (ep->residual && (st = check_matrix(ep->residual, ep->ldr, N)) != FP8BLK_OK) return st;
   if (ep->residual == y && ep->ldr != ldy) return FP8BLK_ERR_INVALID_ARG;
   if (ep->preact && (st = check_matrix(ep->preact, ep->ldp, N)) != FP8BLK_OK) return st;

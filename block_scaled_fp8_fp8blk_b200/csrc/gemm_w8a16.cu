@@ -43,8 +43,8 @@
 //
 // EPI chooses what follows the sums (epilogue.cuh). A promotion thread holds
 // one weight row, i.e. one column of y, for a run of tokens, so kEpiFused has
-// one bias value per thread and reads the residual 16 tokens at a time, 64
-// contiguous bytes per warp and token, before it needs them. kEpiGated makes
+// one bias value per thread; the residual comes through shared memory, 16
+// tokens at a time, one group ahead. kEpiGated makes
 // each 128-row tile of 64 gate rows (TMEM lanes 0-63) and the 64 up rows of
 // the same outputs (lanes 64-127), so expansion, MMAs and promotion run as for
 // any weight; the two warps that hold g and u of the same outputs trade
@@ -88,9 +88,10 @@ struct W8A16Cfg {
   static constexpr int TMEM_COLS = TMEM_USED <= 256 ? 256 : 512;
   static constexpr int XW = EPI == kEpiGated ? 2 * NSUB : 0;  // gate/up warp pairs
   static constexpr int NBAR = 2 * QS + XS + AB + RD + PB * 2 + XW;
-  // Per epilogue warp: 16 tokens x 32 BF16; gated: two buffers of 8 tokens x
-  // 32 FP32 for the trade, the idle one also staging the output.
-  static constexpr int OUT_BYTES = EPI == kEpiGated ? 2 * 8 * 128 : 16 * 64;
+  // Per epilogue warp: 16 tokens x 32 BF16; fused: two of them, each receiving
+  // a group's residual before its output; gated: two buffers of 8 tokens x 32
+  // FP32 for the trade, the idle one also staging the output.
+  static constexpr int OUT_BYTES = EPI == kEpiPlain ? 16 * 64 : 2 * 16 * 64;
   static constexpr size_t SMEM_TILES = static_cast<size_t>(QS) * Q_BYTES +
                                        static_cast<size_t>(XS) * X_BYTES + 4 * NSUB * OUT_BYTES;
   static constexpr size_t SMEM = 1024 + SMEM_TILES + 8 * NBAR + 16;
@@ -296,27 +297,112 @@ __device__ __forceinline__ void stage_and_flush(uint8_t* stg, const float* v, ui
   flush_rows<ROWS>(stg, out, ld, m0, c_first, M, N, lane);
 }
 
-// kEpiFused on 16 tokens m0.. of column n (this lane's; c_first its warp's
-// first column): z = v + bias, kept if asked, y = act(z) + residual.
-__device__ __forceinline__ void fused_group(const FusedEpi& e, float bias, float (&v)[16],
-                                            uint8_t* stg, uint16_t* y, int64_t ldy, int m0,
-                                            int c_first, int M, int N, int lane) {
-  const int n = c_first + lane;
-  uint16_t r[16];
+// The residual of the 16 tokens from m0 on, 32 columns, on its way into a
+// staging buffer (laid out as stage_and_flush lays the output); what lies
+// outside the matrix becomes 0.
+__device__ __forceinline__ void fetch_residual(uint8_t* stg, const uint16_t* res, int64_t ldr, int m0,
+                                               int c_first, int M, int N, int lane) {
+  const int rr = lane >> 1, c0 = c_first + 16 * (lane & 1), m = m0 + rr;
+  const int left = m < M ? N - c0 : 0;  // values of this row from c0 on
+  const uint16_t* src = res + static_cast<int64_t>(m) * ldr + c0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = 0;
-  if (e.residual && n < N) {
-    const uint16_t* rp = e.residual + static_cast<int64_t>(m0) * e.ldr + n;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (m0 + i < M) r[i] = rp[i * e.ldr];
+  for (int i = 0; i < 2; ++i) {
+    const int bytes = 2 * max(0, min(8, left - 8 * i));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     smem_addr(stg + rr * 64 + (lane & 1) * 32 + 16 * i)),
+                 "l"(bytes ? src + 8 * i : res), "r"(bytes)
+                 : "memory");
   }
+}
+
+// kEpiFused, 16 tokens at a time: z = v + bias, kept if asked, y = act(z) +
+// residual. The residual of a group is fetched one group ahead into the
+// staging buffer that the group's output will take (the first one's during the
+// tile's products), so only its shared-memory reads are on the way.
+struct FusedTile {
+  uint8_t* stg;  // two buffers of 1 KB
+  float bias;
+  int group = 0;  // groups so far (parity = buffer)
+};
+
+__device__ __forceinline__ void fused_fetch(FusedTile& t, const FusedEpi& e, int ahead, int m0,
+                                            int c_first, int M, int N, int lane) {
+  if (e.residual && m0 < M)
+    fetch_residual(t.stg + ((t.group + ahead) & 1) * 1024, e.residual, e.ldr, m0, c_first, M, N, lane);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ void fused_group(FusedTile& t, const FusedEpi& e, float (&v)[16],
+                                            uint16_t* y, int64_t ldy, int m0, int c_first, int M,
+                                            int N, int lane) {
+  uint8_t* stg = t.stg + (t.group & 1) * 1024;
+  ++t.group;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] += bias;
-  if (e.preact) stage_and_flush<16>(stg, v, e.preact, e.ldp, m0, c_first, M, N, lane);
+  for (int i = 0; i < 16; ++i) v[i] += t.bias;
+  asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the group ahead
+  __syncwarp();
+  const uint8_t* mine = stg + lane * 2;
+  uint32_t r[8];  // two values each
+  if (e.residual) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = act_value(e.act, v[i]) + bf16_bits_to_f32(r[i]);
+    for (int i = 0; i < 8; ++i)
+      r[i] = *reinterpret_cast<const uint16_t*>(mine + 128 * i) |
+             static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(mine + 128 * i + 64)) << 16;
+  }
+  if (e.preact) {
+    __syncwarp();
+    stage_and_flush<16>(stg, v, e.preact, e.ldp, m0, c_first, M, N, lane);
+  }
+  act_apply(e.act, v);
+  if (e.residual) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] += bf16_lo_to_f32(r[i]);
+      v[2 * i + 1] += bf16_hi_to_f32(r[i]);
+    }
+  }
   stage_and_flush<16>(stg, v, y, ldy, m0, c_first, M, N, lane);
+}
+
+// f(i, v) for the NG groups of 16 tokens of a thread's sums, in order, with one
+// copy of f's code: groups move down to the first registers instead of being
+// indexed (see epilogue.cuh on instruction fetch).
+__device__ __forceinline__ void group_values(const uint64_t* a, float (&v)[16]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * e]), "=f"(v[2 * e + 1]) : "l"(a[e]));
+}
+template <int NG, class F>
+__device__ __forceinline__ void for_groups(uint64_t (&acc)[8 * NG], F f) {
+  float v[16];
+  if constexpr (NG == 8) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      group_values(acc, v);
+      f(i, v);
+      if (i == 3) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc[k] = acc[32 + k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 24; ++k) acc[k] = acc[8 + k];
+      }
+    }
+  } else if constexpr (NG == 4) {
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      group_values(acc, v);
+      f(i, v);
+#pragma unroll
+      for (int k = 0; k < 24; ++k) acc[k] = acc[8 + k];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+      group_values(acc + 8 * i, v);
+      f(i, v);
+    }
+  }
 }
 
 // The trade between the warp that holds g and the warp that holds u of the
@@ -350,13 +436,17 @@ __device__ __forceinline__ bool gated_group(GateTrade& t, const GatedEpi& e, flo
   uint8_t* stg = t.mine + (b ^ 1024);
   if (e.g) stage_and_flush<16>(stg, v, t.is_up ? e.u : e.g, e.ldgu, m0, c_first, M, N, lane);
   const float* got = reinterpret_cast<const float*>(t.theirs + b) + lane;
-  float o[8];
+  float a[8], o[8];  // gates and ups
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float x = got[32 * i];
     const float own = t.is_up ? v[8 + i] : v[i];
-    o[i] = t.is_up ? act_value(e.act, x) * own : act_value(e.act, own) * x;
+    a[i] = t.is_up ? x : own;
+    o[i] = t.is_up ? own : x;
   }
+  act_apply(e.act, a);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] *= a[i];
   stage_and_flush<8>(stg, o, h, ldh, m0 + (t.is_up ? 8 : 0), c_first, M, N, lane);
   return true;
 }
@@ -547,6 +637,7 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + C::TMEM_P +
                               static_cast<uint32_t>(64 * h);
       uint8_t* stg = sOut + ew * C::OUT_BYTES;
+      FusedTile ft{stg, 0.0f};
       GateTrade tr;
       if constexpr (GATED)
         tr = {stg, sOut + (ew ^ 2) * C::OUT_BYTES, &trade[2 * h + (quad & 1)], quad >= 2};
@@ -560,6 +651,10 @@ __global__ void __launch_bounds__(512, 1)
         tile_of<GROUPED>(tile, mtiles, ntiles_total, gm, mt, nt);
         const int m0 = mt * (BT * NSUB), n0 = nt * TILE_N;
         const float* sw_row = sw_of_quad + static_cast<int64_t>(n0 >> 7) * KB;
+        const int nw = n0 + (GATED ? (quad & 1) : quad) * 32;  // first column of this warp
+        if constexpr (EPI == kEpiFused) {
+          if (kb0 == 0 && kb1 == KB) fused_fetch(ft, ep.e, 0, m0 + 64 * h, nw, M, N, lane);
+        }
         uint64_t acc[64];  // acc[32t + p]: tokens 128t + 64h + 2p and 2p + 1
 #pragma unroll
         for (int e = 0; e < 64; ++e) acc[e] = 0ull;
@@ -615,28 +710,24 @@ __global__ void __launch_bounds__(512, 1)
         }
         // Output: sixteen tokens at a time through shared memory as rows of
         // 32 BF16 (this warp's columns of y), then 32-byte stores per lane.
-        const int nw = n0 + (GATED ? (quad & 1) : quad) * 32;  // first column of this warp
-        float bias = 0.0f;
+        uint16_t* yo = reinterpret_cast<uint16_t*>(y);
+        auto first_token = [&](int i) { return m0 + 128 * (i >> 2) + 64 * h + 16 * (i & 3); };
         if constexpr (EPI == kEpiFused) {
-          if (ep.e.bias && nw + lane < N) bias = bf16_bits_to_f32(__ldg(ep.e.bias + nw + lane));
-        }
+          ft.bias = ep.e.bias && nw + lane < N ? bf16_bits_to_f32(__ldg(ep.e.bias + nw + lane)) : 0.0f;
+          for_groups<8>(acc, [&](int i, float(&v)[16]) {
+            fused_fetch(ft, ep.e, 1, i < 7 ? first_token(i + 1) : M, nw, M, N, lane);
+            fused_group(ft, ep.e, v, yo, ldy, first_token(i), nw, M, N, lane);
+          });
+        } else if constexpr (GATED) {
+          for_groups<8>(acc, [&](int i, float(&v)[16]) {
+            ok = ok && gated_group(tr, ep.e, v, yo, ldy, first_token(i), nw, M, N, lane, err);
+          });
+        } else {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
+          for (int i = 0; i < 8; ++i) {
             float v[16];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * e]), "=f"(v[2 * e + 1]) : "l"(acc[32 * t + 8 * g + e]));
-            const int mg = m0 + 128 * t + 64 * h + 16 * g;
-            uint16_t* yo = reinterpret_cast<uint16_t*>(y);
-            if constexpr (EPI == kEpiFused) {
-              fused_group(ep.e, bias, v, stg, yo, ldy, mg, nw, M, N, lane);
-            } else if constexpr (GATED) {
-              ok = ok && gated_group(tr, ep.e, v, yo, ldy, mg, nw, M, N, lane, err);
-            } else {
-              stage_and_flush<16>(stg, v, yo, ldy, mg, nw, M, N, lane);
-            }
+            group_values(acc + 8 * i, v);
+            stage_and_flush<16>(stg, v, yo, ldy, first_token(i), nw, M, N, lane);
           }
         }
       }
@@ -646,11 +737,13 @@ __global__ void __launch_bounds__(512, 1)
       const int t = (warp - 8) >> 2;  // token sub-tile
       const int quad = warp & 3;
       const float* sw_of_quad = sw;
+      const int ew = warp - 8;
+      uint8_t* stg = sOut + ew * C::OUT_BYTES;
+      FusedTile ft{stg, 0.0f};
       GateTrade tr;
       if constexpr (GATED) {
         if (quad >= 2) sw_of_quad = ep.e.s_up;
-        const int ew = warp - 8;
-        tr = {sOut + ew * C::OUT_BYTES, sOut + (ew ^ 2) * C::OUT_BYTES, &trade[quad & 1], quad >= 2};
+        tr = {stg, sOut + (ew ^ 2) * C::OUT_BYTES, &trade[quad & 1], quad >= 2};
       }
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + C::TMEM_P;
       int j = 0;
@@ -663,6 +756,11 @@ __global__ void __launch_bounds__(512, 1)
         tile_of<GROUPED>(tile, mtiles, ntiles_total, gm, tm, tn);
         const int m0 = tm * (BT * NSUB), n0 = tn * TILE_N;
         const float* sw_row = sw_of_quad + static_cast<int64_t>(n0 >> 7) * KB;
+        const int mt = m0 + t * BT;
+        const int nw = n0 + (GATED ? (quad & 1) : quad) * 32;  // first column of this warp
+        if constexpr (EPI == kEpiFused) {
+          if (kb0 == 0 && kb1 == KB) fused_fetch(ft, ep.e, 0, mt, nw, M, N, lane);
+        }
         uint64_t acc[BT / 2];
 #pragma unroll
         for (int e = 0; e < BT / 2; ++e) acc[e] = 0ull;
@@ -719,26 +817,23 @@ __global__ void __launch_bounds__(512, 1)
         // weight row (column of y) per lane. Sixteen tokens at a time go
         // through shared memory as rows of 32 BF16, so that each lane then
         // stores 16 contiguous values (32 bytes) of one row of y.
-        const int mt = m0 + t * BT;
-        const int nw = n0 + (GATED ? (quad & 1) : quad) * 32;  // first column of this warp
-        uint8_t* stg = sOut + (warp - 8) * C::OUT_BYTES;
-        float bias = 0.0f;
+        uint16_t* yo = reinterpret_cast<uint16_t*>(y);
         if constexpr (EPI == kEpiFused) {
-          if (ep.e.bias && nw + lane < N) bias = bf16_bits_to_f32(__ldg(ep.e.bias + nw + lane));
-        }
+          ft.bias = ep.e.bias && nw + lane < N ? bf16_bits_to_f32(__ldg(ep.e.bias + nw + lane)) : 0.0f;
+          for_groups<BT / 16>(acc, [&](int i, float(&v)[16]) {
+            fused_fetch(ft, ep.e, 1, i + 1 < BT / 16 ? mt + 16 * (i + 1) : M, nw, M, N, lane);
+            fused_group(ft, ep.e, v, yo, ldy, mt + 16 * i, nw, M, N, lane);
+          });
+        } else if constexpr (GATED) {
+          for_groups<BT / 16>(acc, [&](int i, float(&v)[16]) {
+            ok = ok && gated_group(tr, ep.e, v, yo, ldy, mt + 16 * i, nw, M, N, lane, err);
+          });
+        } else {
 #pragma unroll
-        for (int g = 0; g < BT / 16; ++g) {
-          float v[16];
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * e]), "=f"(v[2 * e + 1]) : "l"(acc[8 * g + e]));
-          uint16_t* yo = reinterpret_cast<uint16_t*>(y);
-          if constexpr (EPI == kEpiFused) {
-            fused_group(ep.e, bias, v, stg, yo, ldy, mt + 16 * g, nw, M, N, lane);
-          } else if constexpr (GATED) {
-            ok = ok && gated_group(tr, ep.e, v, yo, ldy, mt + 16 * g, nw, M, N, lane, err);
-          } else {
-            stage_and_flush<16>(stg, v, yo, ldy, mt + 16 * g, nw, M, N, lane);
+          for (int i = 0; i < BT / 16; ++i) {
+            float v[16];
+            group_values(acc + 8 * i, v);
+            stage_and_flush<16>(stg, v, yo, ldy, mt + 16 * i, nw, M, N, lane);
           }
         }
       }

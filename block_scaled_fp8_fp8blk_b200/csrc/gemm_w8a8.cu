@@ -116,6 +116,13 @@ __device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
 
+// Adds two BF16 values to a pair of FP32 ones.
+__device__ __forceinline__ void add_bf16x2(uint64_t& v, uint32_t b) {
+  float lo, hi;
+  unpack2(v, lo, hi);
+  v = pack_f32x2(lo + bf16_lo_to_f32(b), hi + bf16_hi_to_f32(b));
+}
+
 // Stores the staged 32 x 64 block at (row r0, column base): by TMA up to
 // column n_tma, the last < 8 columns of a ragged N by plain stores.
 __device__ __forceinline__ void store_staged(const CUtensorMap* map, const uint8_t* stage,
@@ -327,11 +334,17 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
                        col0, r0, m, M, N, n_tma);
         }
 #pragma unroll
-        for (int p = 0; p < 32; ++p) {
-          float g0, g1, u0, u1;
-          unpack2(acc[p], g0, g1);
-          unpack2(acc[32 + p], u0, u1);
-          acc[p] = pack_f32x2(act_value(ep.e.act, g0) * u0, act_value(ep.e.act, g1) * u1);
+        for (int c = 0; c < 4; ++c) {
+          float v[16];
+#pragma unroll
+          for (int p = 0; p < 8; ++p) unpack2(acc[8 * c + p], v[2 * p], v[2 * p + 1]);
+          act_apply(ep.e.act, v);
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            float u0, u1;
+            unpack2(acc[32 + 8 * c + p], u0, u1);
+            acc[8 * c + p] = pack_f32x2(v[2 * p] * u0, v[2 * p + 1] * u1);
+          }
         }
         if (lane == 0) tma_store_wait_read<0>();
         __syncwarp();
@@ -345,34 +358,21 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
           if constexpr (EPI == kEpiFused) {
             const FusedEpi& e = ep.e;
             uint4 r[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) r[c] = make_uint4(0u, 0u, 0u, 0u);
             if (e.residual && m < M) {
               const uint16_t* rr = e.residual + static_cast<int64_t>(m) * e.ldr + base;
 #pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                r[c] = make_uint4(0u, 0u, 0u, 0u);
-                if (base + 8 * c + 8 <= N) {
-                  r[c] = *reinterpret_cast<const uint4*>(rr + 8 * c);
-                } else if (base + 8 * c < N) {
-                  uint16_t t8[8];
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) t8[i] = base + 8 * c + i < N ? rr[8 * c + i] : uint16_t{0};
-                  r[c] = make_uint4(t8[0] | (t8[1] << 16), t8[2] | (t8[3] << 16),
-                                    t8[4] | (t8[5] << 16), t8[6] | (t8[7] << 16));
-                }
-              }
-            } else {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) r[c] = make_uint4(0u, 0u, 0u, 0u);
+              for (int c = 0; c < 8; ++c) r[c] = load_bf16x8(rr + 8 * c, N - base - 8 * c);
             }
             if (e.bias) {
 #pragma unroll
-              for (int p = 0; p < 32; ++p) {
-                const int n = base + 2 * p;
-                float lo, hi;
-                unpack2(v[p], lo, hi);
-                lo += n < N ? bf16_bits_to_f32(__ldg(e.bias + n)) : 0.0f;
-                hi += n + 1 < N ? bf16_bits_to_f32(__ldg(e.bias + n + 1)) : 0.0f;
-                v[p] = pack_f32x2(lo, hi);
+              for (int c = 0; c < 8; ++c) {
+                const uint4 b = load_bf16x8(e.bias + base + 8 * c, N - base - 8 * c);
+                add_bf16x2(v[4 * c + 0], b.x);
+                add_bf16x2(v[4 * c + 1], b.y);
+                add_bf16x2(v[4 * c + 2], b.z);
+                add_bf16x2(v[4 * c + 3], b.w);
               }
             }
             if (e.preact) {
@@ -383,15 +383,22 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
                            lane, base, r0, m, M, N, n_tma);
             }
 #pragma unroll
-            for (int p = 0; p < 32; ++p) {
-              const uint32_t rw = p % 4 == 0   ? r[p / 4].x
-                                  : p % 4 == 1 ? r[p / 4].y
-                                  : p % 4 == 2 ? r[p / 4].z
-                                               : r[p / 4].w;
-              float lo, hi;
-              unpack2(v[p], lo, hi);
-              v[p] = pack_f32x2(act_value(e.act, lo) + bf16_lo_to_f32(rw),
-                                act_value(e.act, hi) + bf16_hi_to_f32(rw));
+            for (int c = 0; c < 4; ++c) {
+              float f[16];
+#pragma unroll
+              for (int p = 0; p < 8; ++p) unpack2(v[8 * c + p], f[2 * p], f[2 * p + 1]);
+              act_apply(e.act, f);
+#pragma unroll
+              for (int p = 0; p < 8; ++p) v[8 * c + p] = pack_f32x2(f[2 * p], f[2 * p + 1]);
+            }
+            if (e.residual) {
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                add_bf16x2(v[4 * c + 0], r[c].x);
+                add_bf16x2(v[4 * c + 1], r[c].y);
+                add_bf16x2(v[4 * c + 2], r[c].z);
+                add_bf16x2(v[4 * c + 3], r[c].w);
+              }
             }
           }
           if (lane == 0) tma_store_wait_read<0>();

@@ -324,7 +324,7 @@ typedef enum fp8blk_activation {
 /* What follows a linear's product: z = x . dequant(W)^T + bias,
  * y = act(z) + residual. Null pointers leave a part out. */
 typedef struct fp8blk_epilogue {
-  const void* bias;       /* BF16 [N] or NULL; 2-byte aligned */
+  const void* bias;       /* BF16 [N] or NULL */
   int32_t activation;     /* an fp8blk_activation */
   const void* residual;   /* BF16 [M][ldr] or NULL; ldr >= N, ldr % 8 == 0; may be y
                              itself (same pointer, ldr == ldy), must not overlap it otherwise */
