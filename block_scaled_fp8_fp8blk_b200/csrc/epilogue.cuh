@@ -7,9 +7,10 @@
 // and the identity are max(z, lo) with lo = 0 and -infinity; gelu(z) = z
 // Phi(z) with the normal distribution function Phi. So three cases cover the
 // five names, chosen by a branch that is uniform over the grid. All of it is
-// computed in FP32 from the FP32 product; exp and the division use the fast
-// forms, whose error (a few units of 2^-23, growing with |z| through the
-// exponent) is far below half a BF16 step.
+// computed in FP32 from the FP32 product; 2^x and 1/x are the approximate
+// instructions, whose error (a few units of 2^-23, growing with the exponent's
+// magnitude) is far below half a BF16 step; their subnormal results and
+// arguments count as 0.
 //
 // What bounds this code inside a GEMM is instruction fetch: a thread holds 64
 // to 128 sums in registers, so the code is unrolled that many times and run
@@ -31,9 +32,11 @@ enum ActKind : int { kActMax = 0, kActLogistic = 1, kActNormal = 2 };
 
 struct ActParams {
   int kind;
-  float c1, c3;  // kActLogistic: z s(c1 z + c3 z^3)
+  float c1, c3;  // kActLogistic: z s(c1 z + c3 z^3), both times -log2(e)
   float lo;      // kActMax: max(z, lo)
 };
+
+constexpr float kLog2e = 1.4426950408889634f;
 
 inline bool valid_activation(int a) { return a >= FP8BLK_ACT_NONE && a <= FP8BLK_ACT_SILU; }
 
@@ -42,10 +45,21 @@ inline ActParams act_params(int a) {
     case FP8BLK_ACT_RELU: return {kActMax, 0.0f, 0.0f, 0.0f};
     case FP8BLK_ACT_GELU: return {kActNormal, 0.0f, 0.0f, 0.0f};
     case FP8BLK_ACT_GELU_TANH:  // 2 sqrt(2/pi), and 0.044715 of it
-      return {kActLogistic, 1.5957691216057308f, 0.07135481282673f, 0.0f};
-    case FP8BLK_ACT_SILU: return {kActLogistic, 1.0f, 0.0f, 0.0f};
+      return {kActLogistic, -kLog2e * 1.5957691216057308f, -kLog2e * 0.07135481282673f, 0.0f};
+    case FP8BLK_ACT_SILU: return {kActLogistic, -kLog2e, 0.0f, 0.0f};
   }
   return {kActMax, 0.0f, 0.0f, -INFINITY};
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // Phi(z) = 1 - Phi(-z), and for x = |z| / sqrt 2 the tail Phi(-|z|) = erfc(x) / 2
@@ -55,7 +69,7 @@ inline ActParams act_params(int a) {
 // is 0 in FP32.
 __device__ __forceinline__ float act_normal(float z) {
   const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __fdividef(1.0f, fmaf(0.6f, x, 1.0f));
+  const float t = fast_rcp(fmaf(0.6f, x, 1.0f));
   float p = -0.09208156913518906f;
   p = fmaf(p, t, 0.4119424819946289f);
   p = fmaf(p, t, -0.6444502472877502f);
@@ -64,14 +78,15 @@ __device__ __forceinline__ float act_normal(float z) {
   p = fmaf(p, t, 0.29160067439079285f);
   p = fmaf(p, t, 0.33724918961524963f);
   p = fmaf(p, t, 0.3385600745677948f);
-  const float tail = 0.5f * t * p * __expf(-x * x);
+  const float tail = 0.5f * t * p * fast_exp2(-kLog2e * x * x);
   return z < 0.0f ? tail : 1.0f - tail;
 }
 
-// s(c1 z + c3 z^3). Beyond |z| = 100 the logistic is exactly 0 or 1 in FP32
-// (exp(100) overflows to infinity), so z is clamped there: z^3 stays finite.
+// The logistic, 1 / (1 + 2^(c1 z + c3 z^3)). Beyond |z| = 100 it is exactly 0 or 1
+// in FP32 (the power overflows to infinity), so z is clamped there and z^3 stays
+// finite.
 __device__ __forceinline__ float act_logistic(const ActParams& a, float zc) {
-  return __fdividef(1.0f, 1.0f + __expf(-zc * fmaf(a.c3, zc * zc, a.c1)));
+  return fast_rcp(1.0f + fast_exp2(zc * fmaf(a.c3, zc * zc, a.c1)));
 }
 
 __device__ __forceinline__ float act_value(const ActParams& a, float z) {
@@ -101,29 +116,15 @@ __device__ __forceinline__ float act_slope(const ActParams& a, float z, float& v
     const float zc = fminf(fmaxf(z, -100.0f), 100.0f);
     const float s = act_logistic(a, zc);
     value = z * s;
-    return fmaf(zc * s * (1.0f - s), fmaf(3.0f * a.c3, zc * zc, a.c1), s);
+    return fmaf(zc * s * (1.0f - s), (-1.0f / kLog2e) * fmaf(3.0f * a.c3, zc * zc, a.c1), s);
   }
   if (a.kind == kActNormal) {
     const float cdf = act_normal(z);
     value = z * cdf;
-    return fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z), cdf);
+    return fmaf(z * 0.39894228040143268f, fast_exp2(-0.5f * kLog2e * z * z), cdf);
   }
   value = fmaxf(z, a.lo);
   return z > a.lo ? 1.0f : 0.0f;
-}
-
-// Eight BF16 values p[0..8) of a row of which n (possibly <= 0, possibly more
-// than 8) exist, as four words; missing ones are 0. p is 16-byte aligned.
-__device__ __forceinline__ uint4 load_bf16x8(const uint16_t* p, int n) {
-  if (n >= 8) return *reinterpret_cast<const uint4*>(p);
-  uint64_t lo = 0, hi = 0;
-#pragma unroll 1
-  for (int i = 0; i < n; ++i) {
-    const uint64_t v = static_cast<uint64_t>(p[i]) << (16 * (i & 3));
-    if (i < 4) lo |= v; else hi |= v;
-  }
-  return make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
-                    static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32));
 }
 
 // What a GEMM does with its FP32 sums.
@@ -160,7 +161,9 @@ struct EpiParams {};
 
 template <>
 struct EpiParams<kEpiFused> {
-  CUtensorMap tm_pre;  // store map of z (only where the kernel stores by TMA)
+  // Where the kernel moves rows by TMA: the store map of z and the load map of
+  // the residual.
+  CUtensorMap tm_pre, tm_res;
   FusedEpi e;
 };
 

@@ -44,14 +44,14 @@
 // EPI chooses what follows the sums (epilogue.cuh). A promotion thread holds
 // one weight row, i.e. one column of y, for a run of tokens, so kEpiFused has
 // one bias value per thread; the residual comes through shared memory, 16
-// tokens at a time, one group ahead. kEpiGated makes
-// each 128-row tile of 64 gate rows (TMEM lanes 0-63) and the 64 up rows of
-// the same outputs (lanes 64-127), so expansion, MMAs and promotion run as for
-// any weight; the two warps that hold g and u of the same outputs trade
-// halves of each 16-token group through shared memory (FP32) and each stores
-// act(g) * u of eight tokens. The split costs nothing per slab, where two
-// accumulators in one thread would have halved the tokens that share an
-// expansion. Split (stream-K) tiles get the same treatment in the fix-up.
+// tokens at a time, one group ahead. kEpiGated makes each 128-row tile of 64
+// gate rows and the 64 up rows of the same outputs, and the expansion puts
+// them into the TMEM lanes so that each warp's lanes 0-15 are gate rows and its
+// lanes 16-31 the up rows of the same 16 outputs: expansion, MMAs and promotion
+// run as for any weight, and g and u meet by a shuffle within the warp. The
+// split costs nothing per slab, where two accumulators in one thread would have
+// halved the tokens that share an expansion. Split (stream-K) tiles get the
+// same treatment in the fix-up.
 #include <cuda_bf16.h>
 
 #include "epilogue.cuh"
@@ -86,12 +86,10 @@ struct W8A16Cfg {
   static constexpr int TMEM_P = 64 * AB;        // PB buffers x BT columns
   static constexpr int TMEM_USED = TMEM_P + PB * BT;
   static constexpr int TMEM_COLS = TMEM_USED <= 256 ? 256 : 512;
-  static constexpr int XW = EPI == kEpiGated ? 2 * NSUB : 0;  // gate/up warp pairs
-  static constexpr int NBAR = 2 * QS + XS + AB + RD + PB * 2 + XW;
-  // Per epilogue warp: 16 tokens x 32 BF16; fused: two of them, each receiving
-  // a group's residual before its output; gated: two buffers of 8 tokens x 32
-  // FP32 for the trade, the idle one also staging the output.
-  static constexpr int OUT_BYTES = EPI == kEpiPlain ? 16 * 64 : 2 * 16 * 64;
+  static constexpr int NBAR = 2 * QS + XS + AB + RD + PB * 2;
+  // Per epilogue warp: 16 tokens x 32 BF16, the output's staging or (fused) one
+  // of two buffers for the residual.
+  static constexpr int OUT_BYTES = (EPI == kEpiFused ? 2 : 1) * 16 * 64;
   static constexpr size_t SMEM_TILES = static_cast<size_t>(QS) * Q_BYTES +
                                        static_cast<size_t>(XS) * X_BYTES + 4 * NSUB * OUT_BYTES;
   static constexpr size_t SMEM = 1024 + SMEM_TILES + 8 * NBAR + 16;
@@ -191,13 +189,15 @@ struct Schedule {
 // One warpgroup expands the slabs j = eg, eg + NEXP, ... of its CTA: thread r
 // (TMEM lane r) turns weight row r's 128 codes into 64 bf16x2 words and
 // stores them with tcgen05.st into A buffer j % AB.
-template <class C, int NSUB>
+template <class C, int NSUB, bool GATED>
 __device__ __forceinline__ void expand_slabs(int eg, int total_slabs, const uint8_t* sQ,
                                              uint32_t tmem, uint64_t* qfull, uint64_t* qempty,
                                              uint64_t* afull, uint64_t* done, unsigned* err) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quad = warp & 3;
-  const int r = quad * 32 + lane;  // weight row within the tile == TMEM lane
+  // Weight row within the tile that goes to this thread's TMEM lane; gated:
+  // rows 0-63 of a slab are gate rows, 64-127 up rows.
+  const int r = GATED ? (lane & 16) * 4 + quad * 16 + (lane & 15) : quad * 32 + lane;
   const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
   for (int j = eg; j < total_slabs; j += C::NEXP) {
     const int qs = j % C::QS;
@@ -258,48 +258,55 @@ __device__ __forceinline__ void tile_of(int t, int mtiles, int ntiles_total, int
 }
 
 // ------------------------------------------------------------------- output
-// A warp holds 16 tokens x 32 columns of BF16 output staged as rows of 32
-// values: each lane stores 16 contiguous values (32 bytes) of one row.
-// ROWS = 8: 16 bytes per lane.
-template <int ROWS>
-__device__ __forceinline__ void flush_rows(const uint8_t* stg, uint16_t* out, int64_t ld, int m0,
-                                           int c_first, int M, int N, int lane) {
-  constexpr int LPR = 32 / ROWS;    // lanes per row
-  constexpr int VALS = 32 / LPR;    // values per lane
-  const int rr = lane / LPR, hh = lane % LPR;
-  const uint8_t* src = stg + rr * 64 + hh * VALS * 2;
-  const int m = m0 + rr, c0 = c_first + VALS * hh;
-  if (m < M && c0 < N) {
-    uint16_t* dst = out + static_cast<int64_t>(m) * ld + c0;
-    if (c0 + VALS <= N) {
-#pragma unroll
-      for (int i = 0; i < VALS / 8; ++i)
-        reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(src)[i];
-    } else {
-      for (int c = 0; c < N - c0; ++c) dst[c] = reinterpret_cast<const uint16_t*>(src)[c];
-    }
-  }
-  __syncwarp();  // the buffer may be written again
-}
-
-// Stages n tokens (n <= 16) of this lane's column and stores them.
-template <int ROWS>
-__device__ __forceinline__ void stage_and_flush(uint8_t* stg, const float* v, uint16_t* out,
-                                                int64_t ld, int m0, int c_first, int M, int N,
+// Plain: 16 tokens x 32 columns staged as rows of 32 BF16, then each lane
+// stores 16 contiguous values (32 bytes) of one row of y.
+__device__ __forceinline__ void stage_and_flush(uint8_t* stg, const float (&v)[16], uint16_t* y,
+                                                int64_t ldy, int m0, int c_first, int M, int N,
                                                 int lane) {
 #pragma unroll
-  for (int e = 0; e < ROWS; e += 2) {
+  for (int e = 0; e < 16; e += 2) {
     const uint32_t b2 = cvt_bf16x2(v[e + 1], v[e]);
     *reinterpret_cast<uint16_t*>(stg + e * 64 + lane * 2) = static_cast<uint16_t>(b2 & 0xFFFFu);
     *reinterpret_cast<uint16_t*>(stg + (e + 1) * 64 + lane * 2) = static_cast<uint16_t>(b2 >> 16);
   }
   __syncwarp();
-  flush_rows<ROWS>(stg, out, ld, m0, c_first, M, N, lane);
+  const int rr = lane >> 1, hh = lane & 1;
+  const uint8_t* src = stg + rr * 64 + hh * 32;
+  const int m = m0 + rr, c0 = c_first + 16 * hh;
+  if (m < M && c0 < N) {
+    uint16_t* dst = y + static_cast<int64_t>(m) * ldy + c0;
+    if (c0 + 16 <= N) {
+      reinterpret_cast<uint4*>(dst)[0] = reinterpret_cast<const uint4*>(src)[0];
+      reinterpret_cast<uint4*>(dst)[1] = reinterpret_cast<const uint4*>(src)[1];
+    } else {
+      for (int c = 0; c < N - c0; ++c) dst[c] = reinterpret_cast<const uint16_t*>(src)[c];
+    }
+  }
+  __syncwarp();  // the next group overwrites the buffer
+}
+
+// With an epilogue: T values of one column, p pointing at the first of them, ld
+// apart, of which only the first `rows` exist; 64 (gated: 32) contiguous bytes
+// per warp and token. (Words of two tokens through shared memory and 8-byte
+// stores took longer: 10.7 against 9.0 thousand cycles per 256-token tile.)
+template <int T>
+__device__ __forceinline__ void store_column(uint16_t* p, int64_t ld, const float* v, int rows) {
+  if (rows >= T) {
+#pragma unroll
+    for (int e = 0; e < T; e += 2) {
+      const uint32_t b2 = cvt_bf16x2(v[e + 1], v[e]);
+      p[e * ld] = static_cast<uint16_t>(b2 & 0xFFFFu);
+      p[(e + 1) * ld] = static_cast<uint16_t>(b2 >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < T; ++e)
+      if (e < rows) p[e * ld] = static_cast<uint16_t>(cvt_bf16x2(0.0f, v[e]));
+  }
 }
 
 // The residual of the 16 tokens from m0 on, 32 columns, on its way into a
-// staging buffer (laid out as stage_and_flush lays the output); what lies
-// outside the matrix becomes 0.
+// buffer of 16 rows of 64 bytes; what lies outside the matrix becomes 0.
 __device__ __forceinline__ void fetch_residual(uint8_t* stg, const uint16_t* res, int64_t ldr, int m0,
                                                int c_first, int M, int N, int lane) {
   const int rr = lane >> 1, c0 = c_first + 16 * (lane & 1), m = m0 + rr;
@@ -316,9 +323,8 @@ __device__ __forceinline__ void fetch_residual(uint8_t* stg, const uint16_t* res
 }
 
 // kEpiFused, 16 tokens at a time: z = v + bias, kept if asked, y = act(z) +
-// residual. The residual of a group is fetched one group ahead into the
-// staging buffer that the group's output will take (the first one's during the
-// tile's products), so only its shared-memory reads are on the way.
+// residual. The residual of a group is fetched one group ahead (the first one's
+// during the tile's products), so only its shared-memory reads are on the way.
 struct FusedTile {
   uint8_t* stg;  // two buffers of 1 KB
   float bias;
@@ -335,33 +341,22 @@ __device__ __forceinline__ void fused_fetch(FusedTile& t, const FusedEpi& e, int
 __device__ __forceinline__ void fused_group(FusedTile& t, const FusedEpi& e, float (&v)[16],
                                             uint16_t* y, int64_t ldy, int m0, int c_first, int M,
                                             int N, int lane) {
-  uint8_t* stg = t.stg + (t.group & 1) * 1024;
+  const uint8_t* mine = t.stg + (t.group & 1) * 1024 + lane * 2;
   ++t.group;
+  const int n = c_first + lane, rows = n < N ? M - m0 : 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] += t.bias;
-  asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the group ahead
-  __syncwarp();
-  const uint8_t* mine = stg + lane * 2;
-  uint32_t r[8];  // two values each
-  if (e.residual) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      r[i] = *reinterpret_cast<const uint16_t*>(mine + 128 * i) |
-             static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(mine + 128 * i + 64)) << 16;
-  }
-  if (e.preact) {
-    __syncwarp();
-    stage_and_flush<16>(stg, v, e.preact, e.ldp, m0, c_first, M, N, lane);
-  }
+  if (e.preact) store_column<16>(e.preact + static_cast<int64_t>(m0) * e.ldp + n, e.ldp, v, rows);
   act_apply(e.act, v);
   if (e.residual) {
+    asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the group ahead
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[2 * i] += bf16_lo_to_f32(r[i]);
-      v[2 * i + 1] += bf16_hi_to_f32(r[i]);
-    }
+    for (int i = 0; i < 16; ++i)
+      v[i] += bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(mine + 64 * i));
+    __syncwarp();  // read before the buffer's next fetch
   }
-  stage_and_flush<16>(stg, v, y, ldy, m0, c_first, M, N, lane);
+  store_column<16>(y + static_cast<int64_t>(m0) * ldy + n, ldy, v, rows);
 }
 
 // f(i, v) for the NG groups of 16 tokens of a thread's sums, in order, with one
@@ -405,50 +400,26 @@ __device__ __forceinline__ void for_groups(uint64_t (&acc)[8 * NG], F f) {
   }
 }
 
-// The trade between the warp that holds g and the warp that holds u of the
-// same 32 outputs (kEpiGated), 16 tokens at a time: each warp gives the half
-// that the other finishes (the gate's warp finishes tokens 0-7, the up's warp
-// 8-15), alternating between two buffers, with one barrier that both arrive on
-// and wait for. After a warp's wait for trade k, its partner has read trade
-// k - 1 (it read it before arriving for k), so the other buffer is free for
-// staging and then for trade k + 1.
-struct GateTrade {
-  uint8_t* mine;
-  uint8_t* theirs;
-  uint64_t* bar;
-  bool is_up;
-  int count = 0;
-};
-
-// act(g) * u of 16 tokens m0..; v holds g or u of this lane's column. Returns
-// false when the partner never arrived (a time-out, reported).
-__device__ __forceinline__ bool gated_group(GateTrade& t, const GatedEpi& e, float (&v)[16],
-                                            uint16_t* h, int64_t ldh, int m0, int c_first, int M,
-                                            int N, int lane, unsigned* err) {
-  const int b = (t.count & 1) * 1024;
-  float* give = reinterpret_cast<float*>(t.mine + b) + lane;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) give[32 * i] = t.is_up ? v[i] : v[8 + i];
-  __syncwarp();
-  if (lane == 0) mbar_arrive(t.bar);
-  if (!mbar_wait_warp(t.bar, static_cast<uint32_t>(t.count & 1), err, kErrWaitEpilogue)) return false;
-  ++t.count;
-  uint8_t* stg = t.mine + (b ^ 1024);
-  if (e.g) stage_and_flush<16>(stg, v, t.is_up ? e.u : e.g, e.ldgu, m0, c_first, M, N, lane);
-  const float* got = reinterpret_cast<const float*>(t.theirs + b) + lane;
-  float a[8], o[8];  // gates and ups
+// kEpiGated on 16 tokens m0..: lanes 0-15 hold g and lanes 16-31 u of the
+// outputs n0 .. n0 + 15. Each lane trades eight tokens with lane ^ 16 and finishes
+// the other eight: lanes 0-15 the first, lanes 16-31 the last.
+__device__ __forceinline__ void gated_group(const GatedEpi& e, float (&v)[16], uint16_t* h,
+                                            int64_t ldh, int m0, int n0, int M, int N, int lane) {
+  const bool is_up = lane >= 16;
+  const int n = n0 + (lane & 15), rows = n < N ? M - m0 : 0;
+  if (e.g) store_column<16>((is_up ? e.u : e.g) + static_cast<int64_t>(m0) * e.ldgu + n, e.ldgu, v, rows);
+  float a[8], b[8];  // gates and ups of this lane's eight tokens
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float x = got[32 * i];
-    const float own = t.is_up ? v[8 + i] : v[i];
-    a[i] = t.is_up ? x : own;
-    o[i] = t.is_up ? own : x;
+    const float got = __shfl_xor_sync(0xFFFFFFFFu, is_up ? v[i] : v[8 + i], 16);
+    a[i] = is_up ? got : v[i];
+    b[i] = is_up ? v[8 + i] : got;
   }
   act_apply(e.act, a);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] *= a[i];
-  stage_and_flush<8>(stg, o, h, ldh, m0 + (t.is_up ? 8 : 0), c_first, M, N, lane);
-  return true;
+  for (int i = 0; i < 8; ++i) b[i] *= a[i];
+  const int first = is_up ? 8 : 0;
+  store_column<8>(h + static_cast<int64_t>(m0 + first) * ldh + n, ldh, b, rows - first);
 }
 
 template <int BT, int NSUB, bool GROUPED, int EPI>
@@ -474,8 +445,7 @@ __global__ void __launch_bounds__(512, 1)
   uint64_t* afull = xfull + C::XS;     // A buffer written      (4 expansion warps)
   uint64_t* done = afull + C::AB;      // item's MMAs complete  (1 commit)
   uint64_t* pempty = done + C::RD;     // partial consumed      (4 or 8 epilogue warps)
-  uint64_t* trade = pempty + C::PB * 2;  // gate/up trade      (2 warps), one per pair
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(trade + C::XW);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pempty + C::PB * 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int total_slabs = Schedule(KB, ntiles_total, dp_tiles).slabs();
@@ -491,7 +461,6 @@ __global__ void __launch_bounds__(512, 1)
     // One barrier per (partial slot, issuer). NSUB == 2: all eight epilogue
     // warps promote every item.
     for (int b = 0; b < C::PB * 2; ++b) mbar_init(&pempty[b], NSUB == 2 ? 8 : 4);
-    for (int b = 0; b < C::XW; ++b) mbar_init(&trade[b], 2);
     mbar_init_fence();
   }
   if (warp == 2) {
@@ -619,15 +588,15 @@ __global__ void __launch_bounds__(512, 1)
     }
   } else if (wg == 1) {
     setmaxnreg_dec<72>();
-    expand_slabs<C, NSUB>(0, total_slabs, sQ, tmem, qfull, qempty, afull, done, err);
+    expand_slabs<C, NSUB, GATED>(0, total_slabs, sQ, tmem, qfull, qempty, afull, done, err);
   } else {
     setmaxnreg_inc<184>();
     if constexpr (NSUB == 2) {
       // ------------------------------------ promotion/epilogue (two sub-tiles)
       pdl_wait();  // y may still be read by the kernel before
-      const float* sw_of_quad = sw;
+      const float* sw_of_lane = sw;
       if constexpr (GATED) {
-        if ((warp & 3) >= 2) sw_of_quad = ep.e.s_up;
+        if (lane >= 16) sw_of_lane = ep.e.s_up;
       }
       // All eight warps promote every item: warp 8 + 4h + q owns TMEM lane
       // quadrant q and token columns [64h, 64h + 64) of each item's partial,
@@ -638,9 +607,6 @@ __global__ void __launch_bounds__(512, 1)
                               static_cast<uint32_t>(64 * h);
       uint8_t* stg = sOut + ew * C::OUT_BYTES;
       FusedTile ft{stg, 0.0f};
-      GateTrade tr;
-      if constexpr (GATED)
-        tr = {stg, sOut + (ew ^ 2) * C::OUT_BYTES, &trade[2 * h + (quad & 1)], quad >= 2};
       int j = 0;
       bool ok = true;
       bool first_sk = true;  // the next stream-K segment is this CTA's first
@@ -650,8 +616,8 @@ __global__ void __launch_bounds__(512, 1)
         int mt, nt;
         tile_of<GROUPED>(tile, mtiles, ntiles_total, gm, mt, nt);
         const int m0 = mt * (BT * NSUB), n0 = nt * TILE_N;
-        const float* sw_row = sw_of_quad + static_cast<int64_t>(n0 >> 7) * KB;
-        const int nw = n0 + (GATED ? (quad & 1) : quad) * 32;  // first column of this warp
+        const float* sw_row = sw_of_lane + static_cast<int64_t>(n0 >> 7) * KB;
+        const int nw = n0 + quad * (TILE_N / 4);  // first column of this warp
         if constexpr (EPI == kEpiFused) {
           if (kb0 == 0 && kb1 == KB) fused_fetch(ft, ep.e, 0, m0 + 64 * h, nw, M, N, lane);
         }
@@ -720,14 +686,14 @@ __global__ void __launch_bounds__(512, 1)
           });
         } else if constexpr (GATED) {
           for_groups<8>(acc, [&](int i, float(&v)[16]) {
-            ok = ok && gated_group(tr, ep.e, v, yo, ldy, first_token(i), nw, M, N, lane, err);
+            gated_group(ep.e, v, yo, ldy, first_token(i), nw, M, N, lane);
           });
         } else {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             float v[16];
             group_values(acc + 8 * i, v);
-            stage_and_flush<16>(stg, v, yo, ldy, first_token(i), nw, M, N, lane);
+            stage_and_flush(stg, v, yo, ldy, first_token(i), nw, M, N, lane);
           }
         }
       }
@@ -736,15 +702,12 @@ __global__ void __launch_bounds__(512, 1)
       pdl_wait();  // y and the workspace may still be in use by the kernel before
       const int t = (warp - 8) >> 2;  // token sub-tile
       const int quad = warp & 3;
-      const float* sw_of_quad = sw;
-      const int ew = warp - 8;
-      uint8_t* stg = sOut + ew * C::OUT_BYTES;
-      FusedTile ft{stg, 0.0f};
-      GateTrade tr;
+      const float* sw_of_lane = sw;
       if constexpr (GATED) {
-        if (quad >= 2) sw_of_quad = ep.e.s_up;
-        tr = {stg, sOut + (ew ^ 2) * C::OUT_BYTES, &trade[quad & 1], quad >= 2};
+        if (lane >= 16) sw_of_lane = ep.e.s_up;
       }
+      uint8_t* stg = sOut + (warp - 8) * C::OUT_BYTES;
+      FusedTile ft{stg, 0.0f};
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + C::TMEM_P;
       int j = 0;
       bool ok = true;
@@ -755,9 +718,9 @@ __global__ void __launch_bounds__(512, 1)
         int tm, tn;
         tile_of<GROUPED>(tile, mtiles, ntiles_total, gm, tm, tn);
         const int m0 = tm * (BT * NSUB), n0 = tn * TILE_N;
-        const float* sw_row = sw_of_quad + static_cast<int64_t>(n0 >> 7) * KB;
+        const float* sw_row = sw_of_lane + static_cast<int64_t>(n0 >> 7) * KB;
         const int mt = m0 + t * BT;
-        const int nw = n0 + (GATED ? (quad & 1) : quad) * 32;  // first column of this warp
+        const int nw = n0 + quad * (TILE_N / 4);  // first column of this warp
         if constexpr (EPI == kEpiFused) {
           if (kb0 == 0 && kb1 == KB) fused_fetch(ft, ep.e, 0, mt, nw, M, N, lane);
         }
@@ -826,20 +789,20 @@ __global__ void __launch_bounds__(512, 1)
           });
         } else if constexpr (GATED) {
           for_groups<BT / 16>(acc, [&](int i, float(&v)[16]) {
-            ok = ok && gated_group(tr, ep.e, v, yo, ldy, mt + 16 * i, nw, M, N, lane, err);
+            gated_group(ep.e, v, yo, ldy, mt + 16 * i, nw, M, N, lane);
           });
         } else {
 #pragma unroll
           for (int i = 0; i < BT / 16; ++i) {
             float v[16];
             group_values(acc + 8 * i, v);
-            stage_and_flush<16>(stg, v, yo, ldy, mt + 16 * i, nw, M, N, lane);
+            stage_and_flush(stg, v, yo, ldy, mt + 16 * i, nw, M, N, lane);
           }
         }
       }
     } else {
       // One sub-tile: warps 12-15 are the second expansion group (odd slabs).
-      expand_slabs<C, NSUB>(1, total_slabs, sQ, tmem, qfull, qempty, afull, done, err);
+      expand_slabs<C, NSUB, GATED>(1, total_slabs, sQ, tmem, qfull, qempty, afull, done, err);
     }
   }
 
@@ -895,8 +858,9 @@ SplitTiles split_tiles(int64_t ntiles, int64_t KB, int64_t G) {
 // a single CTA were written directly. Launched as a programmatic dependent
 // of the GEMM: it waits for the GEMM grid to complete before it reads a
 // partial.
-// kEpiGated: a tile is 64 outputs, its gate rows 0-63 and up rows 64-127; a
-// thread sums both rows of its output for two of the eight tokens.
+// kEpiGated: a tile is 64 outputs; the gate row of output r is TMEM lane
+// 32 (r / 16) + r % 16, its up row 16 lanes on, and a thread sums both for two
+// of the eight tokens.
 template <int TOK, int EPI>
 __global__ void __launch_bounds__(256) w8a16_streamk_fixup(const __grid_constant__ SplitTiles st,
                                                            const float* __restrict__ part,
@@ -922,13 +886,14 @@ __global__ void __launch_bounds__(256) w8a16_streamk_fixup(const __grid_constant
 #pragma unroll
   for (int u = 0; u < NT; ++u) acc[u] = acc_up[u] = 0.0f;
   for (int c = 0; c < nc; ++c) {
-    const float* p = part + (static_cast<int64_t>(c0 + c) * 2 + (c == 0 ? slot0 : 0)) * (TOK * 128) + r;
+    const float* p = part + (static_cast<int64_t>(c0 + c) * 2 + (c == 0 ? slot0 : 0)) * (TOK * 128) +
+                     (GATED ? 2 * r - (r & 15) : r);
     float v[NT], w[NT];
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
       const int m = mbase + TSTEP * u;
       v[u] = m < TOK && m0 + m < M ? p[m * 128] : 0.0f;
-      if constexpr (GATED) w[u] = m < TOK && m0 + m < M ? p[m * 128 + 64] : 0.0f;
+      if constexpr (GATED) w[u] = m < TOK && m0 + m < M ? p[m * 128 + 16] : 0.0f;
     }
 #pragma unroll
     for (int u = 0; u < NT; ++u) {

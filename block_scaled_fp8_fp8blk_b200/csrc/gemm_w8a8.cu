@@ -42,8 +42,10 @@
 //
 // EPI chooses what follows the sums (epilogue.cuh). kEpiFused adds the bias,
 // applies the activation, adds the residual and rounds once; a thread holds
-// one token row, so it reads its row of the residual in 16-byte pieces, all
-// of a 64-column half before the first is used, and the bias as a broadcast.
+// one token row and 128 columns, finished 64 at a time by one copy of the code;
+// the residual of a half comes by TMA into the staging buffer that then takes
+// the output, the first half's during the tile's products (and the second's
+// into L2), and the sums start from the bias.
 // kEpiGated runs two weights as one: a tile's 256 weight rows are 128 gate
 // rows and the 128 up rows of the same outputs (two 128-row boxes per slab, one
 // issued by each of two lanes of warp 1), and an epilogue warp takes 64 gate
@@ -73,7 +75,7 @@ struct W8A8Cfg {
   static constexpr int EPI_WARPS = 8;
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
   static constexpr int OUT_BYTES = 32 * 128;              // per epilogue warp: 32 rows x 64 BF16
-  static constexpr int NBAR = ST + RD + 2;
+  static constexpr int NBAR = ST + RD + 2 + EPI_WARPS;
   static constexpr size_t SMEM_TILES =
       static_cast<size_t>(ST) * STAGE_BYTES + static_cast<size_t>(EPI_WARPS) * OUT_BYTES;
   static constexpr size_t SMEM = 1024 + SMEM_TILES + 8 * NBAR + 16;
@@ -123,6 +125,12 @@ __device__ __forceinline__ void add_bf16x2(uint64_t& v, uint32_t b) {
   v = pack_f32x2(lo + bf16_lo_to_f32(b), hi + bf16_hi_to_f32(b));
 }
 
+// p[n] and p[n + 1] of the N values of p (n even), missing ones 0.
+__device__ __forceinline__ uint32_t load_bf16x2(const uint16_t* p, int n, int N) {
+  if (n + 1 < N) return __ldg(reinterpret_cast<const uint32_t*>(p + n));
+  return n < N ? __ldg(p + n) : 0u;
+}
+
 // Stores the staged 32 x 64 block at (row r0, column base): by TMA up to
 // column n_tma, the last < 8 columns of a ragged N by plain stores.
 __device__ __forceinline__ void store_staged(const CUtensorMap* map, const uint8_t* stage,
@@ -140,6 +148,14 @@ __device__ __forceinline__ void store_staged(const CUtensorMap* map, const uint8
         reinterpret_cast<const uint16_t*>(srow + (((cl >> 3) ^ (lane & 7)) << 4));
     for (int e = 0; e < N - n_tma; ++e) dst_row[n_tma + e] = src[e];
   }
+}
+
+__device__ __forceinline__ const CUtensorMap* residual_map(const EpiParams<kEpiFused>& ep) {
+  return &ep.tm_res;
+}
+template <int EPI>
+__device__ __forceinline__ const CUtensorMap* residual_map(const EpiParams<EPI>&) {
+  return nullptr;
 }
 
 template <int EPI>
@@ -161,7 +177,8 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
   uint64_t* full = bars;               // stage landed       (2 or 3 producers + tx)
   uint64_t* done = full + C::ST;       // slab's MMAs done   (1 commit)
   uint64_t* pempty = done + C::RD;     // partial consumed   (8 epilogue warps), one per issuer
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pempty + 2);
+  uint64_t* rfull = pempty + 2;        // residual landed    (1 + tx), one per epilogue warp
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rfull + C::EPI_WARPS);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ntiles_n = ntiles_total / mtiles;
@@ -173,6 +190,7 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
     for (int s = 0; s < C::ST; ++s) mbar_init(&full[s], GATED ? 3 : 2);
     for (int b = 0; b < C::RD; ++b) mbar_init(&done[b], 1);
     for (int b = 0; b < 2; ++b) mbar_init(&pempty[b], C::EPI_WARPS);
+    for (int b = 0; b < C::EPI_WARPS; ++b) mbar_init(&rfull[b], 1);
     mbar_init_fence();
   }
   if (warp == 2) {
@@ -270,6 +288,19 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
     uint8_t* srow = stage + lane * 128;
     int j = 0;
     bool ok = true;
+    // Loads the residual of the 32 x 64 block at (r0, base) into the staging
+    // buffer once that buffer's last store has been read out. Two loads per
+    // tile that has rows for this warp, whether or not the columns exist (what
+    // does not is filled with zeros), so the barrier's phase is the half's number.
+    auto load_residual = [&](int base, int r0) {
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_wait_read<0>();
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(&rfull[ew], C::OUT_BYTES);
+        tma_load_2d(stage, residual_map(ep), &rfull[ew], base, r0);
+      }
+    };
     for (int tile = blockIdx.x; tile < ntiles_total && ok; tile += gridDim.x) {
       int mt, nt;
       tile_coords(tile, mtiles, ntiles_n, gm, mt, nt);
@@ -286,6 +317,24 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
       uint64_t acc[64];  // column pairs (gated: 32 of the gate, then 32 of up)
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+      if constexpr (EPI == kEpiFused) {
+        if (ep.e.residual && m0 + quad * 32 < M) {
+          // (The staging buffer serves z first where that is kept.)
+          if (!ep.e.preact) load_residual(col0, m0 + quad * 32);
+          if (lane == 0) tma_prefetch_2d(&ep.tm_res, col0 + 64, m0 + quad * 32);
+        }
+        if (ep.e.bias) {  // the sums start from the bias
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const uint32_t mine = load_bf16x2(ep.e.bias, col0 + 64 * hh + 2 * lane, N);
+#pragma unroll
+            for (int p = 0; p < 32; ++p) {
+              const uint32_t b = __shfl_sync(0xFFFFFFFFu, mine, p);
+              acc[32 * hh + p] = pack_f32x2(bf16_lo_to_f32(b), bf16_hi_to_f32(b));
+            }
+          }
+        }
+      }
       // The two scale factors of a slab are loaded one slab ahead and only
       // multiplied when used, so the product does not wait on the loads.
       float fx = has_cols ? __ldg(sx_col) : 0.0f, fw = has_cols ? __ldg(sw_row) : 0.0f;
@@ -305,9 +354,16 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
         }
         tc_fence_after_sync();
         const uint32_t tp = t_lane + static_cast<uint32_t>((j & 1) * C::BN);
+        // With an epilogue, 16 columns per load: its own registers and two
+        // 32-column loads exceed the budget, and the spills and reloads that
+        // follow land in this loop (512 x 5120 x 51200 without activation:
+        // 225 us against 162). The plain kernel keeps the wider loads (139
+        // against 143).
         if constexpr (GATED) {
-          tmem_axpy2<2>(tp, c, acc);
-          tmem_axpy2<2>(tp + 128u, cu, acc + 32);
+          tmem_axpy2_narrow<2>(tp, c, acc);
+          tmem_axpy2_narrow<2>(tp + 128u, cu, acc + 32);
+        } else if constexpr (EPI == kEpiFused) {
+          tmem_axpy2_narrow<4>(tp, c, acc);
         } else {
           tmem_axpy2<4>(tp, c, acc);
         }
@@ -319,6 +375,7 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
       // Output, 64 columns at a time: the staging buffer's previous store has
       // been read out before it is written again.
       const int r0 = m0 + quad * 32;
+      if (EPI != kEpiPlain && r0 >= M) continue;  // no rows for this warp
       uint16_t* yrow = y + static_cast<int64_t>(m) * ldy;
       if constexpr (GATED) {
         if (ep.e.g) {  // kept pre-activations
@@ -350,60 +407,59 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
         __syncwarp();
         stage_row(srow, lane, acc);
         store_staged(&tm_y, stage, srow, yrow, lane, col0, r0, m, M, N, n_tma);
-      } else {
+      } else if constexpr (EPI == kEpiFused) {
+        const FusedEpi& e = ep.e;
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const int base = col0 + 64 * hh;
           uint64_t* v = acc + 32 * hh;
-          if constexpr (EPI == kEpiFused) {
-            const FusedEpi& e = ep.e;
-            uint4 r[8];
-#pragma unroll
-            for (int c = 0; c < 8; ++c) r[c] = make_uint4(0u, 0u, 0u, 0u);
-            if (e.residual && m < M) {
-              const uint16_t* rr = e.residual + static_cast<int64_t>(m) * e.ldr + base;
-#pragma unroll
-              for (int c = 0; c < 8; ++c) r[c] = load_bf16x8(rr + 8 * c, N - base - 8 * c);
-            }
-            if (e.bias) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                const uint4 b = load_bf16x8(e.bias + base + 8 * c, N - base - 8 * c);
-                add_bf16x2(v[4 * c + 0], b.x);
-                add_bf16x2(v[4 * c + 1], b.y);
-                add_bf16x2(v[4 * c + 2], b.z);
-                add_bf16x2(v[4 * c + 3], b.w);
-              }
-            }
-            if (e.preact) {
-              if (lane == 0) tma_store_wait_read<0>();
-              __syncwarp();
-              stage_row(srow, lane, v);
-              store_staged(&ep.tm_pre, stage, srow, e.preact + static_cast<int64_t>(m) * e.ldp,
-                           lane, base, r0, m, M, N, n_tma);
-            }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              float f[16];
-#pragma unroll
-              for (int p = 0; p < 8; ++p) unpack2(v[8 * c + p], f[2 * p], f[2 * p + 1]);
-              act_apply(e.act, f);
-#pragma unroll
-              for (int p = 0; p < 8; ++p) v[8 * c + p] = pack_f32x2(f[2 * p], f[2 * p + 1]);
-            }
-            if (e.residual) {
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                add_bf16x2(v[4 * c + 0], r[c].x);
-                add_bf16x2(v[4 * c + 1], r[c].y);
-                add_bf16x2(v[4 * c + 2], r[c].z);
-                add_bf16x2(v[4 * c + 3], r[c].w);
-              }
-            }
+          if (e.preact) {
+            if (lane == 0) tma_store_wait_read<0>();
+            __syncwarp();
+            stage_row(srow, lane, v);
+            store_staged(&ep.tm_pre, stage, srow, e.preact + static_cast<int64_t>(m) * e.ldp, lane,
+                         base, r0, m, M, N, n_tma);
+            if (e.residual) load_residual(base, r0);
           }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float f[16];
+#pragma unroll
+            for (int p = 0; p < 8; ++p) unpack2(v[8 * c + p], f[2 * p], f[2 * p + 1]);
+            act_apply(e.act, f);
+#pragma unroll
+            for (int p = 0; p < 8; ++p) v[8 * c + p] = pack_f32x2(f[2 * p], f[2 * p + 1]);
+          }
+          if (e.residual) {
+            if (!mbar_wait_warp(&rfull[ew], static_cast<uint32_t>(hh), err, kErrWaitEpilogue)) {
+              ok = false;
+              break;
+            }
+            // A lane adds its own row's residual, then its output takes the place.
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const uint4 r = *reinterpret_cast<const uint4*>(srow + ((c ^ (lane & 7)) << 4));
+              add_bf16x2(v[4 * c + 0], r.x);
+              add_bf16x2(v[4 * c + 1], r.y);
+              add_bf16x2(v[4 * c + 2], r.z);
+              add_bf16x2(v[4 * c + 3], r.w);
+            }
+          } else {
+            if (lane == 0) tma_store_wait_read<0>();
+            __syncwarp();
+          }
+          stage_row(srow, lane, v);
+          store_staged(&tm_y, stage, srow, yrow, lane, base, r0, m, M, N, n_tma);
+          if (hh == 0 && e.residual && !e.preact) load_residual(base + 64, r0);
+        }
+        if (!ok) break;
+      } else {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int base = col0 + 64 * hh;
           if (lane == 0) tma_store_wait_read<0>();
           __syncwarp();
-          stage_row(srow, lane, v);
+          stage_row(srow, lane, acc + 32 * hh);
           store_staged(&tm_y, stage, srow, yrow, lane, base, r0, m, M, N, n_tma);
         }
       }
@@ -420,9 +476,9 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
   }
 }
 
-// A store map over the columns [0, N rounded down to 8) of a BF16 matrix
-// (none if N < 8).
-bool store_map(CUtensorMap* map, const uint16_t* p, int64_t n_tma, int64_t M, int64_t ld) {
+// A map of 32 x 64 blocks over the first n_tma columns of a BF16 matrix: stores
+// take N rounded down to 8 (none if N < 8), loads all of N.
+bool block_map(CUtensorMap* map, const uint16_t* p, int64_t n_tma, int64_t M, int64_t ld) {
   if (n_tma > 0 && p) return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p, n_tma, M, 2 * ld, 64, 32);
   memset(map, 0, sizeof(*map));
   return true;
@@ -446,13 +502,15 @@ cudaError_t launch_epi(const Launch& L, const uint8_t* qx, int64_t ldqx, const f
   if (!make_tmap_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_UINT8, q, K, N, ldq, 128, kTileN))
     return cudaErrorInvalidValue;
   const int64_t n_tma = N & ~int64_t{7};
-  if (!store_map(&ty, y, n_tma, M, ldy)) return cudaErrorInvalidValue;
+  if (!block_map(&ty, y, n_tma, M, ldy)) return cudaErrorInvalidValue;
   if constexpr (EPI == kEpiFused) {
-    if (!store_map(&ep.tm_pre, ep.e.preact, n_tma, M, ep.e.ldp)) return cudaErrorInvalidValue;
+    if (!block_map(&ep.tm_pre, ep.e.preact, n_tma, M, ep.e.ldp) ||
+        !block_map(&ep.tm_res, ep.e.residual, N, M, ep.e.ldr))
+      return cudaErrorInvalidValue;
   } else if constexpr (EPI == kEpiGated) {
     if (!make_tmap_2d(&ep.tm_up, CU_TENSOR_MAP_DATA_TYPE_UINT8, ep.e.q_up, K, N, ldq, 128, kTileN) ||
-        !store_map(&ep.tm_g, ep.e.g, n_tma, M, ep.e.ldgu) ||
-        !store_map(&ep.tm_u, ep.e.u, n_tma, M, ep.e.ldgu))
+        !block_map(&ep.tm_g, ep.e.g, n_tma, M, ep.e.ldgu) ||
+        !block_map(&ep.tm_u, ep.e.u, n_tma, M, ep.e.ldgu))
       return cudaErrorInvalidValue;
   }
   auto kern = w8a8_gemm_kernel<EPI>;

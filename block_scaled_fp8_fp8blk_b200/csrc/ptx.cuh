@@ -166,6 +166,14 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// Brings the tile into L2 only.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -437,6 +445,19 @@ __device__ __forceinline__ void tmem_axpy2(uint32_t t, float c, uint64_t* acc2) 
     tmem_ld32x32(t + 32u * j, p);
 #pragma unroll
     for (int i = 0; i < 16; ++i) ffma2(acc2[16 * j + i], pack_u32x2(p[2 * i], p[2 * i + 1]), c2);
+  }
+}
+
+// tmem_axpy2 with 16 columns per load: half the registers in flight.
+template <int NCH>
+__device__ __forceinline__ void tmem_axpy2_narrow(uint32_t t, float c, uint64_t* acc2) {
+  const uint64_t c2 = pack_f32x2(c, c);
+#pragma unroll
+  for (int j = 0; j < 2 * NCH; ++j) {
+    uint32_t p[16];
+    tmem_ld32x16(t + 16u * j, p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ffma2(acc2[8 * j + i], pack_u32x2(p[2 * i], p[2 * i + 1]), c2);
   }
 }
 
