@@ -136,8 +136,9 @@ def _round_up(a: int, b: int) -> int:
 
 
 def _stream():
+    """The raw handle of the current stream of the current CUDA device."""
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ld(t) -> int:
@@ -145,7 +146,9 @@ def _ld(t) -> int:
         raise ValueError("expected a 2-D tensor")
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError("expected unit column stride")
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else max(t.shape[1], t.stride(0), 1)
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError("rows overlap: expected a row stride of at least the columns")
+    return max(t.shape[1], t.stride(0), 1)
 
 
 def _padded(rows: int, cols: int, ld: int, dtype, device):
@@ -300,26 +303,36 @@ def streamed_linears(jobs, slots, slot_bytes: int, nslots: int, workspace, compu
 
 
 # ------------------------------------------------- feed-forward operators
-def _matrix(t, shape, dtype, device, what):
-    """Checks a 2-D operand: dtype, shape, device; returns its leading dimension."""
-    if t.dtype != dtype:
+# (Small layers are bound by the host: the checks below read each tensor's
+# properties once, and work out a message only for a refusal.)
+def _matrix(t, rows, cols, dtype, dev, what):
+    """Leading dimension of a 2-D operand [rows, cols] of the dtype on CUDA device dev."""
+    if t.dtype is dtype and t.get_device() == dev and t.shape == (rows, cols):
+        ld, step = t.stride()
+        if step != 1 and cols > 1:
+            raise ValueError(f"{what}: expected unit column stride")
+        if ld >= cols:
+            return ld or 1
+        if rows > 1:
+            raise ValueError(f"{what}: rows overlap (row stride {ld}, {cols} columns)")
+        return cols or 1
+    if t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{what}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{what}: on {t.device}, expected {device}")
-    return _ld(t)
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, expected cuda:{dev}")
+    raise ValueError(f"{what}: expected shape {(rows, cols)}, got {tuple(t.shape)}")
 
 
 def _device(t, what):
-    """The device of the call's tensors: the current CUDA device, whose stream it uses."""
+    """The index of the current CUDA device, on which t must be."""
     import torch
     if not t.is_cuda:
         raise ValueError(f"{what}: expected a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
         raise ValueError(f"{what}: on {t.device}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    return t.device
+    return dev
 
 
 def _activation(name):
@@ -334,31 +347,36 @@ def _dims(t, what):
     return t.shape
 
 
-def _weight(q, s, N, K, device, what):
-    """Checks a block-FP8 weight; returns its codes' leading dimension."""
+def _weight(q, s, N, K, dev, what):
+    """Leading dimension of a block-FP8 weight's codes [N, K], its scales checked."""
     import torch
-    ld = _matrix(q, (N, K), torch.uint8, device, f"{what} codes")
-    if N and K and (tuple(s.shape) != (_cdiv(N, 128), _cdiv(K, 128)) or not s.is_contiguous()):
+    ld = _matrix(q, N, K, torch.uint8, dev, what + " codes")
+    if N and K and not (s.shape == ((N + 127) // 128, (K + 127) // 128) and s.is_contiguous()):
         raise ValueError(f"{what} scales: expected a contiguous [{_cdiv(N, 128)}, {_cdiv(K, 128)}] grid")
-    if s.dtype != torch.float32 or s.device != device:
-        raise ValueError(f"{what} scales: expected float32 on {device}")
+    if s.dtype is not torch.float32 or s.get_device() != dev:
+        raise ValueError(f"{what} scales: expected float32 on cuda:{dev}")
     return ld
 
 
-def _scratch(workspace, need, device):
+def _scratch(workspace, need, dev):
     """(tensor kept alive, pointer, bytes) of a workspace, allocated here if None."""
-    import torch
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous tensor on {device}")
-    if workspace is None:
-        return None, None, 0
+        if not need:
+            return None, None, 0
+        import torch
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        return workspace, workspace.data_ptr(), need
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{dev}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _new(rows, cols, align, dtype, device):
-    return _padded(rows, cols, _round_up(max(cols, 1), align), dtype, device)
+def _new(rows, cols, align, dtype, dev):
+    """A new matrix whose rows are a multiple of align elements apart."""
+    import torch
+    ld = (max(cols, 1) + align - 1) // align * align
+    buf = torch.empty((rows, ld), dtype=dtype, device=dev)
+    return buf if ld == cols else buf[:, :cols]
 
 
 def _linear_epilogue(mode, name, x, q, scale_inv, bias, activation, residual, preact, out, workspace):
@@ -368,20 +386,20 @@ def _linear_epilogue(mode, name, x, q, scale_inv, bias, activation, residual, pr
     M, K = _dims(x, "x")
     N = _dims(q, "q")[0]
     dev = _device(x, "x")
-    ldx = _matrix(x, (M, K), bf16, dev, "x")
+    ldx = _matrix(x, M, K, bf16, dev, "x")
     ldq = _weight(q, scale_inv, N, K, dev, "weight")
     ep = Epilogue(None, act, None, 0, None, 0)
     if bias is not None:
-        if tuple(bias.shape) != (N,) or bias.dtype != bf16 or not bias.is_contiguous() or bias.device != dev:
-            raise ValueError(f"bias: expected {N} contiguous BF16 values on {dev}")
+        if not (bias.shape == (N,) and bias.dtype is bf16 and bias.is_contiguous() and bias.get_device() == dev):
+            raise ValueError(f"bias: expected {N} contiguous BF16 values on cuda:{dev}")
         ep.bias = bias.data_ptr()
     if residual is not None:
-        ep.residual, ep.ldr = residual.data_ptr(), _matrix(residual, (M, N), bf16, dev, "residual")
+        ep.residual, ep.ldr = residual.data_ptr(), _matrix(residual, M, N, bf16, dev, "residual")
     if preact is not None:
-        ep.preact, ep.ldp = preact.data_ptr(), _matrix(preact, (M, N), bf16, dev, "preact")
+        ep.preact, ep.ldp = preact.data_ptr(), _matrix(preact, M, N, bf16, dev, "preact")
     if out is None:
         out = _new(M, N, 8, bf16, dev)
-    ldy = _matrix(out, (M, N), bf16, dev, "out")
+    ldy = _matrix(out, M, N, bf16, dev, "out")
     workspace, ws, ws_len = _scratch(workspace, workspace_size(mode, M, N, K), dev)
     _check(getattr(lib(), name)(x.data_ptr(), ldx, q.data_ptr(), ldq, scale_inv.data_ptr(),
                                 out.data_ptr(), ldy, M, N, K, ctypes.byref(ep), ws, ws_len,
@@ -413,7 +431,7 @@ def _gated_linear(mode, name, x, q_gate, s_gate, q_up, s_up, activation, out, pr
     M, K = _dims(x, "x")
     N = _dims(q_gate, "q_gate")[0]
     dev = _device(x, "x")
-    ldx = _matrix(x, (M, K), bf16, dev, "x")
+    ldx = _matrix(x, M, K, bf16, dev, "x")
     ldq = _weight(q_gate, s_gate, N, K, dev, "gate weight")
     if _weight(q_up, s_up, N, K, dev, "up weight") != ldq:
         raise ValueError("q_gate and q_up: expected one row stride")
@@ -421,12 +439,12 @@ def _gated_linear(mode, name, x, q_gate, s_gate, q_up, s_up, activation, out, pr
     ldgu = 0
     if preact is not None:
         g, u = preact
-        ldgu = _matrix(g, (M, N), bf16, dev, "g")
-        if _matrix(u, (M, N), bf16, dev, "u") != ldgu:
+        ldgu = _matrix(g, M, N, bf16, dev, "g")
+        if _matrix(u, M, N, bf16, dev, "u") != ldgu:
             raise ValueError("g and u: expected one row stride")
     if out is None:
         out = _new(M, N, 8, bf16, dev)
-    ldh = _matrix(out, (M, N), bf16, dev, "out")
+    ldh = _matrix(out, M, N, bf16, dev, "out")
     workspace, ws, ws_len = _scratch(workspace, workspace_size(mode, M, 2 * N, K), dev)
     _check(getattr(lib(), name)(x.data_ptr(), ldx, q_gate.data_ptr(), s_gate.data_ptr(),
                                 q_up.data_ptr(), s_up.data_ptr(), ldq, act, out.data_ptr(), ldh,
@@ -464,14 +482,14 @@ def gated_backward(dh, g, u, activation="silu", out=None):
     bf16 = torch.bfloat16
     M, N = _dims(dh, "dh")
     dev = _device(dh, "dh")
-    lddh = _matrix(dh, (M, N), bf16, dev, "dh")
-    ldgu = _matrix(g, (M, N), bf16, dev, "g")
-    if _matrix(u, (M, N), bf16, dev, "u") != ldgu:
+    lddh = _matrix(dh, M, N, bf16, dev, "dh")
+    ldgu = _matrix(g, M, N, bf16, dev, "g")
+    if _matrix(u, M, N, bf16, dev, "u") != ldgu:
         raise ValueError("g and u: expected one row stride")
     width = 2 * _round_up(N, 128)
     if out is None:
         out = torch.empty((M, width), dtype=bf16, device=dev)
-    ldo = _matrix(out, (M, width), bf16, dev, "out")
+    ldo = _matrix(out, M, width, bf16, dev, "out")
     _check(lib().fp8blk_gated_backward(dh.data_ptr(), lddh, g.data_ptr(), u.data_ptr(), ldgu, act,
                                        out.data_ptr(), ldo, M, N, _stream()), "fp8blk_gated_backward")
     return out
@@ -490,15 +508,15 @@ def epilogue_backward(dy, z=None, activation="none", dz=None, bias_grad=True, wo
     bf16 = torch.bfloat16
     M, N = _dims(dy, "dy")
     dev = _device(dy, "dy")
-    lddy = _matrix(dy, (M, N), bf16, dev, "dy")
+    lddy = _matrix(dy, M, N, bf16, dev, "dy")
     ldz = 0
     if z is not None:
-        ldz = _matrix(z, (M, N), bf16, dev, "z")
+        ldz = _matrix(z, M, N, bf16, dev, "z")
     elif act != 0:
         raise ValueError("z: needed for every activation but none")
     if dz is None:
         dz = dy if act == 0 else _new(M, N, 8, bf16, dev)
-    lddz = _matrix(dz, (M, N), bf16, dev, "dz")
+    lddz = _matrix(dz, M, N, bf16, dev, "dz")
     dbias = torch.empty(N, dtype=torch.float32, device=dev) if bias_grad else None
     need = epilogue_backward_workspace_size(M, N) if bias_grad else 0
     workspace, ws, ws_len = _scratch(workspace, need, dev)
@@ -509,11 +527,11 @@ def epilogue_backward(dy, z=None, activation="none", dz=None, bias_grad=True, wo
     return dz, dbias
 
 
-def _transpose_into(q, s, qt, st, zero_pad):
+def _transpose_into(q, s, ldq, qt, ldqt, st, ldst, zero_pad):
+    """qt and st as addresses."""
     N, K = q.shape
-    _check(lib().fp8blk_transpose_weight(q.data_ptr(), _ld(q), s.data_ptr(), N, K, qt.data_ptr(),
-                                         _ld(qt), st.data_ptr(), _ld(st), zero_pad, _stream()),
-           "fp8blk_transpose_weight")
+    _check(lib().fp8blk_transpose_weight(q.data_ptr(), ldq, s.data_ptr(), N, K, qt, ldqt, st, ldst,
+                                         zero_pad, _stream()), "fp8blk_transpose_weight")
 
 
 def transpose_weight(q, scale_inv, qt=None, st=None):
@@ -522,13 +540,13 @@ def transpose_weight(q, scale_inv, qt=None, st=None):
     import torch
     N, K = _dims(q, "q")
     dev = _device(q, "q")
-    _weight(q, scale_inv, N, K, dev, "weight")
+    ldq = _weight(q, scale_inv, N, K, dev, "weight")
     if qt is None:
         qt = _new(K, N, 16, torch.uint8, dev)
     if st is None:
         st = torch.empty((_cdiv(K, 128), _cdiv(N, 128)), dtype=torch.float32, device=dev)
-    _weight(qt, st, K, N, dev, "transposed weight")
-    _transpose_into(q, scale_inv, qt, st, 0)
+    ldqt = _weight(qt, st, K, N, dev, "transposed weight")
+    _transpose_into(q, scale_inv, ldq, qt.data_ptr(), ldqt, st.data_ptr(), st.shape[1], 0)
     return qt, st
 
 
@@ -539,17 +557,16 @@ def transpose_gated_weights(q_gate, s_gate, q_up, s_up, qt=None, st=None):
     import torch
     N, K = _dims(q_gate, "q_gate")
     dev = _device(q_gate, "q_gate")
-    _weight(q_gate, s_gate, N, K, dev, "gate weight")
-    _weight(q_up, s_up, N, K, dev, "up weight")
+    ldq = (_weight(q_gate, s_gate, N, K, dev, "gate weight"), _weight(q_up, s_up, N, K, dev, "up weight"))
     NB = _cdiv(N, 128)
     Np = 128 * NB
     if qt is None:
         qt = torch.empty((K, 2 * Np), dtype=torch.uint8, device=dev)
     if st is None:
         st = torch.empty((_cdiv(K, 128), 2 * NB), dtype=torch.float32, device=dev)
-    _weight(qt, st, K, 2 * Np, dev, "transposed weight")
+    ldqt = _weight(qt, st, K, 2 * Np, dev, "transposed weight")
     for i, (q, s) in enumerate(((q_gate, s_gate), (q_up, s_up))):
-        _transpose_into(q, s, qt[:, i * Np:(i + 1) * Np], st[:, i * NB:(i + 1) * NB], 1)
+        _transpose_into(q, s, ldq[i], qt.data_ptr() + i * Np, ldqt, st.data_ptr() + 4 * i * NB, 2 * NB, 1)
     return qt, st
 
 
@@ -562,8 +579,8 @@ def linear_grad_weight(dz, x, out=None, accumulate=False, dtype=None):
     M, N = _dims(dz, "dz")
     K = _dims(x, "x")[1]
     dev = _device(dz, "dz")
-    lddz = _matrix(dz, (M, N), bf16, dev, "dz")
-    ldx = _matrix(x, (M, K), bf16, dev, "x")
+    lddz = _matrix(dz, M, N, bf16, dev, "dz")
+    ldx = _matrix(x, M, K, bf16, dev, "x")
     dtype = dtype or (out.dtype if out is not None else f32)
     if dtype not in (bf16, f32):
         raise ValueError(f"dw: expected float32 or bfloat16, got {dtype}")
@@ -571,7 +588,7 @@ def linear_grad_weight(dz, x, out=None, accumulate=False, dtype=None):
         raise ValueError("accumulate: needs a float32 out")
     if out is None:
         out = _new(N, K, 4 if dtype == f32 else 8, dtype, dev)
-    lddw = _matrix(out, (N, K), dtype, dev, "out")
+    lddw = _matrix(out, N, K, dtype, dev, "out")
     _check(lib().fp8blk_linear_grad_weight(dz.data_ptr(), lddz, x.data_ptr(), ldx, out.data_ptr(), lddw,
                                            int(dtype == f32), int(accumulate), M, N, K, _stream()),
            "fp8blk_linear_grad_weight")

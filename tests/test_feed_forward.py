@@ -544,6 +544,10 @@ def test_refusals_of_the_binding():
         fb.gated_linear_w8a16(x.float(), q, s, q, s)
     with pytest.raises(ValueError, match="stride"):
         fb.linear_w8a16_epilogue(x, q, s, residual=normal(g, 200, 4).t())
+    with pytest.raises(ValueError, match="overlap"):
+        fb.linear_w8a16_epilogue(x, q, s, residual=normal(g, 1, 200).expand(4, 200))
+    with pytest.raises(ValueError, match="overlap"):
+        fb.linear_grad_weight(x[:1].expand(4, 256), x)
     with pytest.raises(ValueError, match="z: needed"):
         fb.epilogue_backward(x, activation="gelu")
     with pytest.raises(ValueError, match="accumulate"):

@@ -139,3 +139,12 @@ def test_binding_refuses_host_tensors():
               lambda: fb.linear_grad_weight(x, x)):
         with pytest.raises(ValueError, match="CUDA"):
             f()
+
+
+def test_overlapping_rows_are_refused():
+    """A broadcast tensor has row stride 0: its rows are not [rows, cols] memory."""
+    wide = torch.zeros((1, 128), dtype=torch.bfloat16).expand(4, 128)
+    with pytest.raises(ValueError, match="overlap"):
+        fb._ld(wide)
+    assert fb._ld(torch.zeros((1, 128)).expand(1, 128)) == 128
+    assert fb._ld(torch.zeros((3, 1)).expand(3, 1)) == 1 and fb._ld(torch.zeros((0, 5))) == 5
