@@ -14,15 +14,18 @@
 namespace fp8blk {
 namespace {
 
+__device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
+  v[0] = bf16_lo_to_f32(w.x), v[1] = bf16_hi_to_f32(w.x);
+  v[2] = bf16_lo_to_f32(w.y), v[3] = bf16_hi_to_f32(w.y);
+  v[4] = bf16_lo_to_f32(w.z), v[5] = bf16_hi_to_f32(w.z);
+  v[6] = bf16_lo_to_f32(w.w), v[7] = bf16_hi_to_f32(w.w);
+}
+
 // Eight BF16 values of a row from column c on: one 16-byte load where all
 // eight exist, else the existing ones and zeros.
 __device__ __forceinline__ void load8(const uint16_t* row, int64_t c, int64_t n, float (&v)[8]) {
   if (c + 8 <= n) {
-    const uint4 w = *reinterpret_cast<const uint4*>(row + c);
-    v[0] = bf16_lo_to_f32(w.x), v[1] = bf16_hi_to_f32(w.x);
-    v[2] = bf16_lo_to_f32(w.y), v[3] = bf16_hi_to_f32(w.y);
-    v[4] = bf16_lo_to_f32(w.z), v[5] = bf16_hi_to_f32(w.z);
-    v[6] = bf16_lo_to_f32(w.w), v[7] = bf16_hi_to_f32(w.w);
+    unpack8(*reinterpret_cast<const uint4*>(row + c), v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = c + i < n ? bf16_bits_to_f32(row[c + i]) : 0.0f;
@@ -63,18 +66,47 @@ __global__ void __launch_bounds__(256)
 }
 
 // dz = dy act'(z) and, with SUM, the column sums of the unrounded products. A
-// block takes 256 columns (32 lanes x 8) and a run of rows, eight at a time;
-// each thread sums its rows, the block adds its eight warps in order, and the
-// blocks of one column strip are added in order by column_sum_kernel. So the
-// order of the sum depends on the sizes alone. dz may be dy or z: a thread
-// writes only what it has read.
+// block takes 256 columns (32 lanes x 8) and a run of rows, eight at a time, two
+// steps in flight; each thread sums its rows, the block adds its eight warps in
+// order, and the blocks of one column strip are added in order by
+// column_sum_kernel. So the order of the sum depends on the sizes alone. Four
+// blocks fit an SM (64 registers a thread). dz may be dy or z: a thread writes
+// only what it has read.
 constexpr int kStripCols = 256, kRowsPerStep = 8;
 
+// One row's eight columns: d *= act'(z), stored, summed.
 template <bool SUM>
-__global__ void __launch_bounds__(256)
+__device__ __forceinline__ void epilogue_backward_row(float (&d)[8], const float (&v)[8], bool has_z,
+                                                      const ActParams& act, uint16_t* out, int64_t c,
+                                                      int64_t N, float (&sum)[8]) {
+  if (has_z) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a;
+      d[i] *= act_slope(act, v[i], a);
+    }
+  }
+  if (out) {
+    if (c + 8 <= N) {
+      *reinterpret_cast<uint4*>(out + c) = pack8(d);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i < N) out[c + i] = static_cast<uint16_t>(cvt_bf16x2(0.0f, d[i]));
+    }
+  }
+  if constexpr (SUM) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum[i] += d[i];
+  }
+}
+
+template <bool SUM>
+__global__ void __launch_bounds__(256, 4)
     epilogue_backward_kernel(const uint16_t* dy, int64_t lddy, const uint16_t* z, int64_t ldz,
                              ActParams act, uint16_t* dz, int64_t lddz, float* sums, int64_t M,
                              int64_t N, int64_t rows) {
+  if constexpr (SUM) pdl_launch_dependents();  // column_sum_kernel, which waits for this grid
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * kStripCols + lane * 8;
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * rows;
@@ -82,34 +114,34 @@ __global__ void __launch_bounds__(256)
   float sum[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
-  if (c < N) {
-#pragma unroll 2
-    for (int64_t m = m0 + warp; m < m1; m += kRowsPerStep) {
-      float d[8];
-      load8(dy + m * lddy, c, N, d);
+  auto row_out = [&](int64_t m) { return dz ? dz + m * lddz : nullptr; };
+  int64_t m = m0 + warp;
+  if (c + 8 <= N) {
+    for (; m + kRowsPerStep < m1; m += 2 * kRowsPerStep) {  // two rows: all loads first
+      const int64_t mb = m + kRowsPerStep;
+      const uint4 da = *reinterpret_cast<const uint4*>(dy + m * lddy + c);
+      const uint4 db = *reinterpret_cast<const uint4*>(dy + mb * lddy + c);
+      uint4 za = make_uint4(0u, 0u, 0u, 0u), zb = za;
       if (z) {
-        float v[8];
-        load8(z + m * ldz, c, N, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float a;
-          d[i] *= act_slope(act, v[i], a);
-        }
+        za = *reinterpret_cast<const uint4*>(z + m * ldz + c);
+        zb = *reinterpret_cast<const uint4*>(z + mb * ldz + c);
       }
-      if (dz) {
-        uint16_t* out = dz + m * lddz + c;
-        if (c + 8 <= N) {
-          *reinterpret_cast<uint4*>(out) = pack8(d);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c + i < N) out[i] = static_cast<uint16_t>(cvt_bf16x2(0.0f, d[i]));
-        }
-      }
-      if constexpr (SUM) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum[i] += d[i];
-      }
+      float d[8], v[8];
+      unpack8(da, d);
+      unpack8(za, v);
+      epilogue_backward_row<SUM>(d, v, z != nullptr, act, row_out(m), c, N, sum);
+      unpack8(db, d);
+      unpack8(zb, v);
+      epilogue_backward_row<SUM>(d, v, z != nullptr, act, row_out(mb), c, N, sum);
+    }
+  }
+  if (c < N) {
+#pragma unroll 1
+    for (; m < m1; m += kRowsPerStep) {
+      float d[8], v[8];
+      load8(dy + m * lddy, c, N, d);
+      if (z) load8(z + m * ldz, c, N, v);
+      epilogue_backward_row<SUM>(d, v, z != nullptr, act, row_out(m), c, N, sum);
     }
   }
   if constexpr (SUM) {
@@ -128,6 +160,7 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict__ parts,
                                                          int64_t splits, int64_t N,
                                                          float* __restrict__ out) {
+  pdl_wait();
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   if (n >= N) return;
   float t = 0.0f;
@@ -136,77 +169,84 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const float* __restrict
   out[n] = t;
 }
 
-// Row runs of epilogue_backward_kernel: enough blocks to fill the machine four
-// times (4 x 148), whole steps of eight rows each.
+// Row runs of epilogue_backward_kernel, whole steps of eight rows: about 2368
+// blocks in all, four times what a B200 holds at once (4 x 148), so that the last
+// wave weighs little. (600 blocks, 8 more than fit, took 162 us at 4096 x 25600.)
 struct RowSplit {
   int64_t rows, splits;
 };
 RowSplit row_split(int64_t M, int64_t N) {
-  const int64_t strips = cdiv(N, kStripCols), want = cdiv(592, strips);
+  const int64_t strips = cdiv(N, kStripCols), want = cdiv(2368, strips);
   const int64_t rows = round_up(cdiv(M, want), kRowsPerStep);
   return {rows, cdiv(M, rows)};
 }
 
 // qt[k][n] = q[n][k] for one 128 x 128 block of codes per thread block. A
-// thread transposes 4 x 4 codes in registers; the words cross through shared
-// memory, word (k, n/4) at column (n/4) ^ (k/4): both the writes (lanes along
-// k/4) and the reads (lanes along n/4) then touch 32 different banks. Rows are
-// read and written as whole 128-byte lines.
+// thread takes 4 rows x 16 codes (four 16-byte loads, a warp four whole 128-byte
+// lines at a time), transposes 4 x 4 codes in registers, and the words cross
+// through shared memory: word (k, n / 4) sits in 16-byte chunk (n / 16) ^ (k / 16)
+// of row k, so that the writes (8 values of k / 16, 4 of n / 4) touch 32 different
+// banks and the reads are whole rows, 16 bytes a lane.
 __global__ void __launch_bounds__(256)
     transpose_kernel(const uint8_t* __restrict__ q, int64_t ldq, const float* __restrict__ s,
                      int64_t N, int64_t K, uint8_t* __restrict__ qt, int64_t ldqt,
                      float* __restrict__ st, int64_t ldst, int64_t n_end) {
-  __shared__ uint32_t t[128 * 32];
+  __shared__ __align__(16) uint32_t t[128 * 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t kb = blockIdx.x, nb = blockIdx.y;
-  const int64_t k0 = kb * 128, n0 = nb * 128, k = k0 + 4 * lane;
-  uint32_t w[4][4];
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
+  const int64_t k0 = kb * 128, n0 = nb * 128;
+  {
+    const int r = lane & 3, k16 = lane >> 2;
+    const int64_t k = k0 + 16 * k16, n = n0 + 16 * warp + 4 * r;
+    uint32_t w[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t n = n0 + 4 * (warp + 8 * b) + i;
-      uint32_t v = 0;
-      if (n < N) {
-        const uint8_t* p = q + n * ldq + k;
-        if (k + 4 <= K) {
-          v = *reinterpret_cast<const uint32_t*>(p);
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (n + i < N && k < K) {
+        const uint8_t* p = q + (n + i) * ldq + k;
+        if (k + 16 <= K) {
+          v = *reinterpret_cast<const uint4*>(p);
         } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (k + e < K) v |= static_cast<uint32_t>(p[e]) << (8 * e);
+          uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+          for (int e = 0; k + e < K; ++e) {
+            const uint64_t b = static_cast<uint64_t>(p[e]) << (8 * (e & 7));
+            if (e < 8) lo |= b; else hi |= b;
+          }
+          v = make_uint4(static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32),
+                         static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32));
         }
       }
-      w[b][i] = v;
+      w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+    }
+    const int col = 4 * (warp ^ k16) + r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // Byte e of the four rows' words: pairs of rows interleaved, then halves.
+      const uint32_t a = __byte_perm(w[0][j], w[1][j], 0x5140), c = __byte_perm(w[2][j], w[3][j], 0x5140);
+      const uint32_t d = __byte_perm(w[0][j], w[1][j], 0x7362), f = __byte_perm(w[2][j], w[3][j], 0x7362);
+      uint32_t* o = t + (16 * k16 + 4 * j) * 32 + col;
+      o[0] = __byte_perm(a, c, 0x5410);
+      o[32] = __byte_perm(a, c, 0x7632);
+      o[64] = __byte_perm(d, f, 0x5410);
+      o[96] = __byte_perm(d, f, 0x7632);
     }
   }
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    // 16-bit halves, then bytes: o[e] = byte e of the four rows.
-    const uint32_t a = __byte_perm(w[b][0], w[b][1], 0x5140);  // (0: b0 b1 interleaved) e = 0, 1
-    const uint32_t c = __byte_perm(w[b][2], w[b][3], 0x5140);
-    const uint32_t d = __byte_perm(w[b][0], w[b][1], 0x7362);  // e = 2, 3
-    const uint32_t f = __byte_perm(w[b][2], w[b][3], 0x7362);
-    const int col = (warp + 8 * b) ^ lane;
-    t[(4 * lane + 0) * 32 + col] = __byte_perm(a, c, 0x5410);
-    t[(4 * lane + 1) * 32 + col] = __byte_perm(a, c, 0x7632);
-    t[(4 * lane + 2) * 32 + col] = __byte_perm(d, f, 0x5410);
-    t[(4 * lane + 3) * 32 + col] = __byte_perm(d, f, 0x7632);
-  }
   __syncthreads();
-  const int64_t n = n0 + 4 * lane;
+  const int64_t n = n0 + 16 * (lane & 7);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int kk = warp + 8 * i;
+  for (int i = 0; i < 4; ++i) {
+    const int kk = 4 * warp + (lane >> 3) + 32 * i;
     if (k0 + kk >= K) break;
-    const uint32_t v = t[kk * 32 + (lane ^ (kk >> 2))];
+    const uint4 v = reinterpret_cast<const uint4*>(t)[kk * 8 + ((lane & 7) ^ (kk >> 4))];
     uint8_t* p = qt + (k0 + kk) * ldqt + n;
-    if (n + 4 <= n_end) {
-      *reinterpret_cast<uint32_t*>(p) = v;
+    if (n + 16 <= n_end) {
+      *reinterpret_cast<uint4*>(p) = v;
     } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + e < n_end) p[e] = static_cast<uint8_t>(v >> (8 * e));
+      uint64_t lo = v.x | static_cast<uint64_t>(v.y) << 32, hi = v.z | static_cast<uint64_t>(v.w) << 32;
+#pragma unroll 1
+      for (int e = 0; e < 16 && n + e < n_end; ++e)
+        p[e] = static_cast<uint8_t>((e < 8 ? lo : hi) >> (8 * (e & 7)));
     }
   }
   if (threadIdx.x == 0) st[kb * ldst + nb] = s[nb * gridDim.x + kb];
@@ -285,7 +325,6 @@ fp8blk_status fp8blk_epilogue_backward(const void* dy, int64_t lddy, const void*
   if (M == 0)
     return cuda_status(cudaMemsetAsync(dbias, 0, static_cast<size_t>(N) * sizeof(float), L.stream));
   const RowSplit r = row_split(M, N);
-  if (r.splits > 65535) return FP8BLK_ERR_INVALID_ARG;  // (592 at most)
   const dim3 grid(static_cast<unsigned>(cdiv(N, kStripCols)), static_cast<unsigned>(r.splits));
   const uint16_t* dyp = static_cast<const uint16_t*>(dy);
   const uint16_t* zp = identity ? nullptr : static_cast<const uint16_t*>(z);
@@ -300,9 +339,18 @@ fp8blk_status fp8blk_epilogue_backward(const void* dy, int64_t lddy, const void*
   epilogue_backward_kernel<true><<<grid, 256, 0, L.stream>>>(dyp, lddy, zp, ldz, act, dzp, lddz,
                                                              sums, M, N, r.rows);
   if (cudaGetLastError() != cudaSuccess) return FP8BLK_ERR_CUDA;
-  if (r.splits > 1)
-    column_sum_kernel<<<static_cast<unsigned>(cdiv(N, 256)), 256, 0, L.stream>>>(sums, r.splits, N, dbias);
-  return cuda_status(cudaGetLastError());
+  if (r.splits == 1) return FP8BLK_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(N, 256)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, column_sum_kernel, static_cast<const float*>(sums),
+                                        r.splits, N, dbias));
 }
 
 fp8blk_status fp8blk_transpose_weight(const uint8_t* q, int64_t ldq, const float* scale_inv,

@@ -66,19 +66,21 @@ __device__ __forceinline__ float fast_rcp(float x) {
 // = erfcx(x) exp(-x^2) / 2, which keeps its relative accuracy where 1 + erf
 // would cancel. erfcx(x) is a polynomial in t = 1 / (1 + 0.6 x), fitted to it for
 // 0 <= x <= 10 with equal relative error (3.1e-7; 6e-7 in FP32); beyond, exp(-x^2)
-// is 0 in FP32.
-__device__ __forceinline__ float act_normal(float z) {
+// is 0 in FP32. gauss is exp(-z^2/2).
+__device__ __forceinline__ float act_normal(float z, float& gauss) {
   const float x = fabsf(z) * 0.70710678118654752f;
   const float t = fast_rcp(fmaf(0.6f, x, 1.0f));
-  float p = -0.09208156913518906f;
-  p = fmaf(p, t, 0.4119424819946289f);
-  p = fmaf(p, t, -0.6444502472877502f);
-  p = fmaf(p, t, 0.2837655544281006f);
-  p = fmaf(p, t, 0.07341350615024567f);
-  p = fmaf(p, t, 0.29160067439079285f);
-  p = fmaf(p, t, 0.33724918961524963f);
-  p = fmaf(p, t, 0.3385600745677948f);
-  const float tail = 0.5f * t * p * fast_exp2(-kLog2e * x * x);
+  gauss = fast_exp2(-kLog2e * x * x);
+  // (half the fitted coefficients)
+  float p = 0.5f * -0.09208156913518906f;
+  p = fmaf(p, t, 0.5f * 0.4119424819946289f);
+  p = fmaf(p, t, 0.5f * -0.6444502472877502f);
+  p = fmaf(p, t, 0.5f * 0.2837655544281006f);
+  p = fmaf(p, t, 0.5f * 0.07341350615024567f);
+  p = fmaf(p, t, 0.5f * 0.29160067439079285f);
+  p = fmaf(p, t, 0.5f * 0.33724918961524963f);
+  p = fmaf(p, t, 0.5f * 0.3385600745677948f);
+  const float tail = t * p * gauss;
   return z < 0.0f ? tail : 1.0f - tail;
 }
 
@@ -91,7 +93,10 @@ __device__ __forceinline__ float act_logistic(const ActParams& a, float zc) {
 
 __device__ __forceinline__ float act_value(const ActParams& a, float z) {
   if (a.kind == kActLogistic) return z * act_logistic(a, fminf(fmaxf(z, -100.0f), 100.0f));
-  if (a.kind == kActNormal) return z * act_normal(z);
+  if (a.kind == kActNormal) {
+    float gauss;
+    return z * act_normal(z, gauss);
+  }
   return fmaxf(z, a.lo);
 }
 
@@ -103,7 +108,10 @@ __device__ __forceinline__ void act_apply(const ActParams& a, float (&v)[N]) {
     for (int i = 0; i < N; ++i) v[i] *= act_logistic(a, fminf(fmaxf(v[i], -100.0f), 100.0f));
   } else if (a.kind == kActNormal) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] *= act_normal(v[i]);
+    for (int i = 0; i < N; ++i) {
+      float gauss;
+      v[i] *= act_normal(v[i], gauss);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = fmaxf(v[i], a.lo);
@@ -119,9 +127,10 @@ __device__ __forceinline__ float act_slope(const ActParams& a, float z, float& v
     return fmaf(zc * s * (1.0f - s), (-1.0f / kLog2e) * fmaf(3.0f * a.c3, zc * zc, a.c1), s);
   }
   if (a.kind == kActNormal) {
-    const float cdf = act_normal(z);
+    float gauss;
+    const float cdf = act_normal(z, gauss);
     value = z * cdf;
-    return fmaf(z * 0.39894228040143268f, fast_exp2(-0.5f * kLog2e * z * z), cdf);
+    return fmaf(z * 0.39894228040143268f, gauss, cdf);
   }
   value = fmaxf(z, a.lo);
   return z > a.lo ? 1.0f : 0.0f;
