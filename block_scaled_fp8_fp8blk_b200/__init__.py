@@ -22,7 +22,7 @@ __all__ = [
     "ACTIVATIONS", "Epilogue", "linear_w8a16_epilogue", "linear_w8a8_epilogue",
     "gated_linear_w8a16", "gated_linear_w8a8", "gated_backward", "epilogue_backward",
     "epilogue_backward_workspace_size", "transpose_weight", "transpose_gated_weights",
-    "linear_grad_weight",
+    "linear_grad_weight", "linear_grad_weight_workspace_size",
     "LIB_PATH", "EXPORTS",
 ]
 
@@ -89,7 +89,9 @@ EXPORTS = {
     "fp8blk_epilogue_backward": (_st, [_p, _i64, _p, _i64, _i32, _p, _i64, _p, _i64, _i64, _p, _sz, _p]),
     "fp8blk_epilogue_backward_workspace_size": (_sz, [_i64, _i64]),
     "fp8blk_transpose_weight": (_st, [_p, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _i32, _p]),
-    "fp8blk_linear_grad_weight": (_st, [_p, _i64, _p, _i64, _p, _i64, _i32, _i32, _i64, _i64, _i64, _p]),
+    "fp8blk_linear_grad_weight": (_st, [_p, _i64, _p, _i64, _p, _i64, _i32, _i32, _i64, _i64, _i64, _p,
+                                        _sz, _p]),
+    "fp8blk_linear_grad_weight_workspace_size": (_sz, [_i64, _i64, _i64]),
     "fp8blk_encode_e4m3": (_st, [_p, _i64, _p, _p]),
     "fp8blk_read_device_error": (_st, [ctypes.POINTER(ctypes.c_uint32)]),
     "fp8blk_selftest_wait_timeout": (_st, [_i64, _p]),
@@ -570,7 +572,11 @@ def transpose_gated_weights(q_gate, s_gate, q_up, s_up, qt=None, st=None):
     return qt, st
 
 
-def linear_grad_weight(dz, x, out=None, accumulate=False, dtype=None):
+def linear_grad_weight_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib().fp8blk_linear_grad_weight_workspace_size(M, N, K))
+
+
+def linear_grad_weight(dz, x, out=None, accumulate=False, dtype=None, workspace=None):
     """dw [N, K] = dz^T . x over the tokens of dz BF16 [M, N] and x BF16 [M, K],
     FP32 sums; float32 unless out or dtype says BF16. accumulate adds to a
     float32 out."""
@@ -589,9 +595,10 @@ def linear_grad_weight(dz, x, out=None, accumulate=False, dtype=None):
     if out is None:
         out = _new(N, K, 4 if dtype == f32 else 8, dtype, dev)
     lddw = _matrix(out, N, K, dtype, dev, "out")
+    workspace, ws, ws_len = _scratch(workspace, linear_grad_weight_workspace_size(M, N, K), dev)
     _check(lib().fp8blk_linear_grad_weight(dz.data_ptr(), lddz, x.data_ptr(), ldx, out.data_ptr(), lddw,
-                                           int(dtype == f32), int(accumulate), M, N, K, _stream()),
-           "fp8blk_linear_grad_weight")
+                                           int(dtype == f32), int(accumulate), M, N, K, ws, ws_len,
+                                           _stream()), "fp8blk_linear_grad_weight")
     return out
 
 

@@ -26,6 +26,11 @@
 // A commit stalls its issuer for a few hundred cycles, so stages are released
 // in pairs: one commit per 8 MMAs (1024 cycles of the pair's tensor pipes).
 // Every wait is bounded (kWaitLimitCycles) and reports to the error word.
+//
+// Few tiles and many tokens (a 1024 x 1024 weight is 16 tiles for 74 pairs): given
+// a workspace, the tokens are split into runs, each (tile, run) is a unit of
+// work that stores its FP32 sums there, and grad_join_kernel adds the runs in
+// order.
 #include <cuda_bf16.h>
 
 #include <cstring>
@@ -147,8 +152,8 @@ template <bool FP32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradCfg::THREADS, 1)
     grad_weight_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                        const __grid_constant__ CUtensorMap tm_w, void* __restrict__ dw, int64_t lddw,
-                       int N, int K, int k_tma, int steps, int ktiles, int tiles, int gk,
-                       int accumulate, unsigned* __restrict__ err) {
+                       int N, int K, int k_tma, int all_steps, int run_steps, int run_rows,
+                       int ktiles, int tiles, int gk, int accumulate, unsigned* __restrict__ err) {
   using C = GradCfg;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
@@ -165,6 +170,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradCfg::THREADS, 1)
   const uint32_t rank = cluster_rank();
   const int pair = static_cast<int>(blockIdx.x >> 1), npairs = static_cast<int>(gridDim.x >> 1);
   const int ntiles_n = tiles / ktiles;
+  // Units of work: (tile, run of run_steps stages); one run unless the tokens
+  // are split, and then run r stores at row r * run_rows.
+  const int runs = (all_steps + run_steps - 1) / run_steps, units = tiles * runs;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::ST; ++s) mbar_init(&full[s], 4);
@@ -181,6 +189,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradCfg::THREADS, 1)
   cluster_sync();  // both CTAs' barriers and TMEM exist
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();  // the kernel after this one waits for this grid before it reads dw
 
   if (warp < 2) {
     if (lane < 2) {
@@ -191,11 +200,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradCfg::THREADS, 1)
       tma_prefetch_map(map);
       int j = 0;
       bool ok = true;
-      for (int tile = pair; tile < tiles && ok; tile += npairs) {
+      for (int unit = pair; unit < units && ok; unit += npairs) {
         int kt, nt;
-        tile_coords(tile, ktiles, ntiles_n, gk, kt, nt);
+        tile_coords(unit / runs, ktiles, ntiles_n, gk, kt, nt);
+        const int s0 = unit % runs * run_steps, s1 = min(s0 + run_steps, all_steps);
         const int col = (warp == 0 ? nt : kt) * C::TILE + static_cast<int>(rank) * 128 + lane * 64;
-        for (int s = 0; s < steps; ++s, ++j) {
+        for (int s = s0; s < s1; ++s, ++j) {
           const int stage = j % C::ST;
           if ((stage & 1) == 0 && j >= C::ST) {  // the pair's last use has been read
             if (!mbar_wait(&empty[stage >> 1], static_cast<uint32_t>((j / C::ST - 1) & 1), err,
@@ -222,8 +232,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradCfg::THREADS, 1)
       const uint64_t b0 = sw128_mnmajor_desc(smem_addr(smem + C::OP_BYTES));
       int j = 0, it = 0;
       bool ok = true;
-      for (int tile = pair; tile < tiles && ok; tile += npairs, ++it) {
+      for (int unit = pair; unit < units && ok; unit += npairs, ++it) {
         const int buf = it & 1;
+        const int s0 = unit % runs * run_steps, steps = min(run_steps, all_steps - s0);
         if (it >= 2) {
           if (!mbar_wait(&acc_empty[buf], static_cast<uint32_t>(((it >> 1) - 1) & 1), err, kErrWaitMma)) break;
           tc_fence_after_sync();
@@ -259,9 +270,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradCfg::THREADS, 1)
     constexpr int CW = FP32 ? 32 : 64;       // columns of a 128-byte staging row
     constexpr int EPC = FP32 ? 4 : 8;        // elements of a 16-byte chunk
     int it = 0;
-    for (int tile = pair; tile < tiles; tile += npairs, ++it) {
+    for (int unit = pair; unit < units; unit += npairs, ++it) {
       int kt, nt;
-      tile_coords(tile, ktiles, ntiles_n, gk, kt, nt);
+      tile_coords(unit / runs, ktiles, ntiles_n, gk, kt, nt);
+      const int row_off = unit % runs * run_rows;
       const int buf = it & 1;
       if (!mbar_wait_warp(&acc_full[buf], static_cast<uint32_t>((it >> 1) & 1), err, kErrWaitEpilogue)) break;
       tc_fence_after_sync();
@@ -305,9 +317,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradCfg::THREADS, 1)
         __syncwarp();
         if (lane == 0 && r0 < N && base < k_tma) {
           if (FP32 && accumulate)
-            tma_add_2d(&tm_w, stage, base, r0);
+            tma_add_2d(&tm_w, stage, base, row_off + r0);
           else
-            tma_store_2d(&tm_w, stage, base, r0);
+            tma_store_2d(&tm_w, stage, base, row_off + r0);
           tma_store_commit();
         }
         // The columns of a ragged K past the last whole 16 bytes.
@@ -339,6 +351,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GradCfg::THREADS, 1)
   }
 }
 
+// dw (+)= the sum of the runs, in order; parts is [runs][rows][ld] FP32, four
+// columns per thread, ld a multiple of 4 that covers K.
+template <bool FP32>
+__global__ void __launch_bounds__(256)
+    grad_join_kernel(const float* __restrict__ parts, int runs, int64_t rows, int64_t ld, void* dw,
+                     int64_t lddw, int64_t N, int64_t K, int accumulate) {
+  pdl_wait();
+  const int64_t per = ld / 4, i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t n = i / per, k = i % per * 4;
+  if (n >= N) return;
+  const float* p = parts + n * ld + k;
+  float4 a = *reinterpret_cast<const float4*>(p);
+#pragma unroll 4
+  for (int r = 1; r < runs; ++r) {
+    const float4 b = *reinterpret_cast<const float4*>(p + r * rows * ld);
+    a.x += b.x, a.y += b.y, a.z += b.z, a.w += b.w;
+  }
+  const float v[4] = {a.x, a.y, a.z, a.w};
+  if constexpr (FP32) {
+    float* w = static_cast<float*>(dw) + n * lddw + k;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (k + e < K) w[e] = accumulate ? w[e] + v[e] : v[e];
+  } else {
+    uint16_t* w = static_cast<uint16_t*>(dw) + n * lddw + k;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (k + e < K) w[e] = static_cast<uint16_t>(cvt_bf16x2(0.0f, v[e]));
+  }
+}
+
+// How the tokens are split: runs of whole stages, chosen from the sizes alone (for
+// the 74 CTA pairs of a B200; the sums do not depend on how many there are). Runs
+// are at least kMinRunSteps stages (512 tokens) long, and all units run at once.
+// Measured, whole -> split with runs of at least 256 tokens, 1024 x 1024 weights:
+// 512 tokens 14.3 -> 16.4 us, 1024 16.4 -> 18.4, 2048 20.5 -> 18.4, 4096 30.7 -> 22.5;
+// 256 x 256, 4096 tokens 30.7 -> 16.4.
+constexpr int64_t kGradPairs = 74, kMinRunSteps = 8;
+struct TokenSplit {
+  int64_t run_steps, runs;
+};
+TokenSplit token_split(int64_t M, int64_t N, int64_t K) {
+  const int64_t tiles = cdiv(N, GradCfg::TILE) * cdiv(K, GradCfg::TILE), steps = cdiv(M, GradCfg::BT);
+  int64_t runs = kGradPairs / tiles;
+  if (runs > steps / kMinRunSteps) runs = steps / kMinRunSteps;
+  if (runs < 2) return {steps, 1};
+  const int64_t run_steps = cdiv(steps, runs);
+  return {run_steps, cdiv(steps, run_steps)};
+}
+
 // Pairs that can be resident at once (queried once per device and form).
 template <bool FP32>
 cudaError_t resident_pairs(int num_sms, int* pairs) {
@@ -366,20 +428,25 @@ cudaError_t resident_pairs(int num_sms, int* pairs) {
 // Output columns (x) whose operand columns a raster group may keep in L2.
 constexpr int64_t kRasterBytesGrad = 48ll << 20;
 
+// The product of N x K sums into [N][ldw] at w (FP32 or BF16), or, split into
+// runs, into [runs][run_rows][ldw] FP32.
 template <bool FP32>
 cudaError_t launch_grad(const Launch& L, const uint16_t* dz, int64_t lddz, const uint16_t* x,
-                        int64_t ldx, void* dw, int64_t lddw, bool accumulate, int64_t M, int64_t N,
-                        int64_t K) {
+                        int64_t ldx, void* w, int64_t ldw, bool accumulate, int64_t M, int64_t N,
+                        int64_t K, const TokenSplit& split, int64_t run_rows) {
   using C = GradCfg;
   CUtensorMap ta, tb, tw;
   if (!make_tmap_2d(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dz, N, M, 2 * lddz, 64, C::BT) ||
       !make_tmap_2d(&tb, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, K, M, 2 * ldx, 64, C::BT))
     return cudaErrorInvalidValue;
   constexpr int kEsz = FP32 ? 4 : 2;
-  const int64_t k_tma = K & ~int64_t{16 / kEsz - 1};  // whole 16-byte chunks
+  // A run's rows and columns are padded to what the stores write.
+  const int64_t k_out = split.runs > 1 ? ldw : K;
+  const int64_t rows_out = split.runs > 1 ? split.runs * run_rows : N;
+  const int64_t k_tma = k_out & ~int64_t{16 / kEsz - 1};  // whole 16-byte chunks
   if (k_tma > 0) {
     if (!make_tmap_2d(&tw, FP32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                      dw, k_tma, N, kEsz * lddw, 128 / kEsz, 32))
+                      w, k_tma, rows_out, kEsz * ldw, 128 / kEsz, 32))
       return cudaErrorInvalidValue;
   } else {
     memset(&tw, 0, sizeof(tw));
@@ -391,18 +458,42 @@ cudaError_t launch_grad(const Launch& L, const uint16_t* dz, int64_t lddz, const
   e = resident_pairs<FP32>(L.num_sms, &pairs);
   if (e != cudaSuccess) return e;
   const int64_t ktiles = cdiv(K, C::TILE), tiles = ktiles * cdiv(N, C::TILE), steps = cdiv(M, C::BT);
-  if (tiles * steps > 0x7FFFFFFFLL) return cudaErrorInvalidValue;  // 32-bit counters
-  if (tiles < pairs) pairs = static_cast<int>(tiles);
+  const int64_t units = tiles * split.runs;
+  if (tiles * steps > 0x7FFFFFFFLL || rows_out > 0x7FFFFFFFLL) return cudaErrorInvalidValue;  // 32-bit counters
+  if (units < pairs) pairs = static_cast<int>(units);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = L.stream;
-  return cudaLaunchKernelEx(&cfg, kern, ta, tb, tw, dw, lddw, static_cast<int>(N),
-                            static_cast<int>(K), static_cast<int>(k_tma), static_cast<int>(steps),
+  return cudaLaunchKernelEx(&cfg, kern, ta, tb, tw, w, ldw, static_cast<int>(N),
+                            static_cast<int>(k_out), static_cast<int>(k_tma), static_cast<int>(steps),
+                            static_cast<int>(split.run_steps), static_cast<int>(run_rows),
                             static_cast<int>(ktiles), static_cast<int>(tiles),
                             raster_group(ktiles, C::TILE * M * 2, kRasterBytesGrad),
                             accumulate ? 1 : 0, L.err);
+}
+
+int64_t run_rows_of(int64_t N) { return round_up(N, GradCfg::TILE); }
+
+cudaError_t launch_split_grad(const Launch& L, const uint16_t* dz, int64_t lddz, const uint16_t* x,
+                              int64_t ldx, void* dw, int64_t lddw, bool fp32, bool accumulate,
+                              int64_t M, int64_t N, int64_t K, const TokenSplit& split, float* ws) {
+  const int64_t rows = run_rows_of(N), ld = round_up(K, 4);
+  cudaError_t e = launch_grad<true>(L, dz, lddz, x, ldx, ws, ld, false, M, N, K, split, rows);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(cdiv(N * (ld / 4), 256)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fp32 ? grad_join_kernel<true> : grad_join_kernel<false>,
+                            static_cast<const float*>(ws), static_cast<int>(split.runs), rows, ld, dw,
+                            lddw, N, K, accumulate ? 1 : 0);
 }
 
 }  // namespace
@@ -410,10 +501,20 @@ cudaError_t launch_grad(const Launch& L, const uint16_t* dz, int64_t lddz, const
 
 using namespace fp8blk;
 
-extern "C" fp8blk_status fp8blk_linear_grad_weight(const void* dz, int64_t lddz, const void* x,
-                                                   int64_t ldx, void* dw, int64_t lddw,
-                                                   int32_t dw_fp32, int32_t accumulate, int64_t M,
-                                                   int64_t N, int64_t K, fp8blk_stream stream) {
+extern "C" {
+
+size_t fp8blk_linear_grad_weight_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  const TokenSplit s = token_split(M, N, K);
+  return s.runs < 2 ? 0
+                    : static_cast<size_t>(s.runs) * static_cast<size_t>(run_rows_of(N)) *
+                          static_cast<size_t>(round_up(K, 4)) * sizeof(float);
+}
+
+fp8blk_status fp8blk_linear_grad_weight(const void* dz, int64_t lddz, const void* x, int64_t ldx,
+                                        void* dw, int64_t lddw, int32_t dw_fp32, int32_t accumulate,
+                                        int64_t M, int64_t N, int64_t K, void* workspace,
+                                        size_t workspace_bytes, fp8blk_stream stream) {
   if (M < 0 || N < 0 || K < 0) return FP8BLK_ERR_INVALID_ARG;
   if ((dw_fp32 != 0 && dw_fp32 != 1) || (accumulate != 0 && accumulate != 1) ||
       (accumulate && !dw_fp32))
@@ -437,7 +538,15 @@ extern "C" fp8blk_status fp8blk_linear_grad_weight(const void* dz, int64_t lddz,
   }
   const uint16_t* a = static_cast<const uint16_t*>(dz);
   const uint16_t* b = static_cast<const uint16_t*>(x);
-  return cuda_status(dw_fp32
-                         ? launch_grad<true>(L, a, lddz, b, ldx, dw, lddw, accumulate != 0, M, N, K)
-                         : launch_grad<false>(L, a, lddz, b, ldx, dw, lddw, false, M, N, K));
+  TokenSplit split = token_split(M, N, K);
+  const size_t need = fp8blk_linear_grad_weight_workspace_size(M, N, K);
+  if (need && workspace && workspace_bytes >= need && aligned(workspace, 256))
+    return cuda_status(launch_split_grad(L, a, lddz, b, ldx, dw, lddw, dw_fp32 != 0, accumulate != 0,
+                                         M, N, K, split, static_cast<float*>(workspace)));
+  split = {cdiv(M, GradCfg::BT), 1};
+  return cuda_status(
+      dw_fp32 ? launch_grad<true>(L, a, lddz, b, ldx, dw, lddw, accumulate != 0, M, N, K, split, 0)
+              : launch_grad<false>(L, a, lddz, b, ldx, dw, lddw, false, M, N, K, split, 0));
 }
+
+}  // extern "C"

@@ -442,19 +442,29 @@ FP8BLK_EXPORT fp8blk_status fp8blk_transpose_weight(const uint8_t* q, int64_t ld
 
 /* ---------------------------------------------------------------------------
  * Weight gradient of a linear: dw[n][k] = sum_m dz[m][n] * x[m][k], BF16
- * operands, FP32 sums in token order of whole 64-token steps.
+ * operands, FP32 sums in an order that depends on the sizes (and on whether a
+ * workspace was given) alone.
  *   dz : BF16 [M][lddz], lddz >= N; x : BF16 [M][ldx], ldx >= K      (input)
  *   dw : float (dw_fp32 = 1) or BF16 (dw_fp32 = 0) [N][lddw], lddw >= K (output)
  *   accumulate : 1 adds the sums to dw (FP32 only), 0 overwrites it
+ *   workspace : optional, 256-byte aligned, scratch: with
+ *          fp8blk_linear_grad_weight_workspace_size(M, N, K) bytes (0 where it
+ *          would not help) a weight of few tiles has its tokens split over the
+ *          GPU. NULL or a smaller one runs every tile whole.
  * lddz, ldx % 8 == 0; lddw % 4 == 0 (FP32) or % 8 == 0 (BF16). M = 0 sets dw
- * to 0, or leaves it with accumulate. No workspace.
+ * to 0, or leaves it with accumulate.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
  * ------------------------------------------------------------------------- */
 FP8BLK_EXPORT fp8blk_status fp8blk_linear_grad_weight(const void* dz, int64_t lddz, const void* x,
                                                       int64_t ldx, void* dw, int64_t lddw,
                                                       int32_t dw_fp32, int32_t accumulate,
                                                       int64_t M, int64_t N, int64_t K,
+                                                      void* workspace, size_t workspace_bytes,
                                                       fp8blk_stream stream);
+
+/* Workspace bytes of fp8blk_linear_grad_weight. Pure host function; 0 for
+ * negative sizes, and where no workspace is used. */
+FP8BLK_EXPORT size_t fp8blk_linear_grad_weight_workspace_size(int64_t M, int64_t N, int64_t K);
 
 /* Workspace bytes for a linear: mode 0 = W8A16, 1 = W8A8. Pure host function;
  * returns 0 for an invalid mode or negative sizes. */

@@ -367,7 +367,7 @@ def test_transpose_weight(N, K):
 
 
 GRAD_SHAPES = [(1, 8, 8), (1, 256, 256), (5, 1, 1), (16, 640, 512), (63, 257, 130), (64, 128, 384), (65, 300, 72),
-               (77, 1000, 1000), (200, 2048, 640), (512, 1280, 2048), (1030, 520, 264), (4096, 384, 640)]
+               (77, 1000, 1000), (200, 2048, 640), (512, 1280, 2048), (1030, 520, 264), (4096, 384, 640), (2050, 257, 129), (20000, 40, 72)]
 
 
 @pytest.mark.parametrize("M,N,K", GRAD_SHAPES)
@@ -403,6 +403,12 @@ def test_linear_grad_weight_edges():
     first = fb.linear_grad_weight(dz, x)
     for _ in range(4):
         assert torch.equal(fb.linear_grad_weight(dz, x), first)
+    # split over the tokens or whole: the same sums, in another order
+    dz, x = normal(g, 1500, 520), normal(g, 1500, 300)
+    assert fb.linear_grad_weight_workspace_size(1500, 520, 300) > 0
+    split = fb.linear_grad_weight(dz, x)
+    whole = fb.linear_grad_weight(dz, x, workspace=torch.empty(0, dtype=torch.uint8, device=DEV))
+    within(split, whole.double(), (1500 / 8 + 16) * 2.0 ** -22 * (dz.double().abs().T @ x.double().abs()), "split")
 
 
 # ---------------------------------------------------------- used together

@@ -117,8 +117,8 @@ def test_transpose_weight_validation(lib):
 
 def test_linear_grad_weight_validation(lib):
     M, N, K = 64, 200, 304
-    names = "dz lddz x ldx dw lddw fp32 add M N K st".split()
-    call = caller(lib.fp8blk_linear_grad_weight, names, (P, N, P, K, P, K, 1, 0, M, N, K, None))
+    names = "dz lddz x ldx dw lddw fp32 add M N K ws wsb st".split()
+    call = caller(lib.fp8blk_linear_grad_weight, names, (P, N, P, K, P, K, 1, 0, M, N, K, None, 0, None))
     assert call(M=-1) == 1 and call(fp32=2) == 1 and call(add=2) == 1
     assert call(fp32=0, add=1) == 1                                # sums are added in FP32 only
     assert call(dz=None) == 1 and call(x=None) == 1 and call(dw=None) == 1
@@ -148,3 +148,15 @@ def test_overlapping_rows_are_refused():
         fb._ld(wide)
     assert fb._ld(torch.zeros((1, 128)).expand(1, 128)) == 128
     assert fb._ld(torch.zeros((3, 1)).expand(3, 1)) == 1 and fb._ld(torch.zeros((0, 5))) == 5
+
+
+def test_linear_grad_weight_workspace_size(lib):
+    """A workspace where few 256 x 256 tiles meet many tokens: runs of at least
+    eight 64-token stages, all (tile, run) units at once on 74 pairs of SMs."""
+    size = fb.linear_grad_weight_workspace_size
+    assert size(4096, 25600, 5120) == 0 and size(200, 256, 256) == 0 and size(-1, 8, 8) == 0
+    assert size(2048, 1024, 1024) == 4 * 1024 * 1024 * 4        # 16 tiles: 4 runs of 8 stages
+    assert size(1023, 256, 256) == 2 * 256 * 256 * 4            # 16 stages: 2 runs of 8
+    assert size(960, 256, 256) == 0                             # 15 stages
+    assert size(4096, 300, 130) == 8 * 512 * 132 * 4            # rows and columns padded
+    assert size(1 << 20, 1, 1) == 74 * 256 * 4 * 4 and size(4096, 0, 130) == 0
