@@ -328,9 +328,9 @@ def _matrix(t, rows, cols, dtype, dev, what):
 def _device(t, what):
     """The index of the current CUDA device, on which t must be."""
     import torch
-    if not t.is_cuda:
-        raise ValueError(f"{what}: expected a CUDA tensor")
     dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{what}: expected a CUDA tensor")
     if dev != torch.cuda.current_device():
         raise ValueError(f"{what}: on {t.device}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
@@ -352,17 +352,23 @@ def _dims(t, what):
 def _weight(q, s, N, K, dev, what):
     """Leading dimension of a block-FP8 weight's codes [N, K], its scales checked."""
     import torch
-    ld = _matrix(q, N, K, torch.uint8, dev, what + " codes")
+    _scales(s, N, K, dev, what)
+    return _matrix(q, N, K, torch.uint8, dev, what + " codes")
+
+
+def _scales(s, N, K, dev, what):
+    import torch
     if N and K and not (s.shape == ((N + 127) // 128, (K + 127) // 128) and s.is_contiguous()):
         raise ValueError(f"{what} scales: expected a contiguous [{_cdiv(N, 128)}, {_cdiv(K, 128)}] grid")
     if s.dtype is not torch.float32 or s.get_device() != dev:
         raise ValueError(f"{what} scales: expected float32 on cuda:{dev}")
-    return ld
 
 
-def _scratch(workspace, need, dev):
-    """(tensor kept alive, pointer, bytes) of a workspace, allocated here if None."""
+def _scratch(workspace, size, dims, dev):
+    """(tensor kept alive, pointer, bytes) of a workspace; if None, one of
+    size(*dims) bytes allocated here."""
     if workspace is None:
+        need = size(*dims)
         if not need:
             return None, None, 0
         import torch
@@ -374,11 +380,19 @@ def _scratch(workspace, need, dev):
 
 
 def _new(rows, cols, align, dtype, dev):
-    """A new matrix whose rows are a multiple of align elements apart."""
+    """A new matrix whose rows are a multiple of align elements apart, and its
+    leading dimension."""
     import torch
     ld = (max(cols, 1) + align - 1) // align * align
     buf = torch.empty((rows, ld), dtype=dtype, device=dev)
-    return buf if ld == cols else buf[:, :cols]
+    return (buf if ld == cols else buf[:, :cols]), ld
+
+
+def _output(out, rows, cols, align, dtype, dev, what="out"):
+    """out and its leading dimension, made here if None."""
+    if out is None:
+        return _new(rows, cols, align, dtype, dev)
+    return out, _matrix(out, rows, cols, dtype, dev, what)
 
 
 def _linear_epilogue(mode, name, x, q, scale_inv, bias, activation, residual, preact, out, workspace):
@@ -399,10 +413,8 @@ def _linear_epilogue(mode, name, x, q, scale_inv, bias, activation, residual, pr
         ep.residual, ep.ldr = residual.data_ptr(), _matrix(residual, M, N, bf16, dev, "residual")
     if preact is not None:
         ep.preact, ep.ldp = preact.data_ptr(), _matrix(preact, M, N, bf16, dev, "preact")
-    if out is None:
-        out = _new(M, N, 8, bf16, dev)
-    ldy = _matrix(out, M, N, bf16, dev, "out")
-    workspace, ws, ws_len = _scratch(workspace, workspace_size(mode, M, N, K), dev)
+    out, ldy = _output(out, M, N, 8, bf16, dev)
+    workspace, ws, ws_len = _scratch(workspace, workspace_size, (mode, M, N, K), dev)
     _check(getattr(lib(), name)(x.data_ptr(), ldx, q.data_ptr(), ldq, scale_inv.data_ptr(),
                                 out.data_ptr(), ldy, M, N, K, ctypes.byref(ep), ws, ws_len,
                                 _stream()), name)
@@ -444,10 +456,8 @@ def _gated_linear(mode, name, x, q_gate, s_gate, q_up, s_up, activation, out, pr
         ldgu = _matrix(g, M, N, bf16, dev, "g")
         if _matrix(u, M, N, bf16, dev, "u") != ldgu:
             raise ValueError("g and u: expected one row stride")
-    if out is None:
-        out = _new(M, N, 8, bf16, dev)
-    ldh = _matrix(out, M, N, bf16, dev, "out")
-    workspace, ws, ws_len = _scratch(workspace, workspace_size(mode, M, 2 * N, K), dev)
+    out, ldh = _output(out, M, N, 8, bf16, dev)
+    workspace, ws, ws_len = _scratch(workspace, workspace_size, (mode, M, 2 * N, K), dev)
     _check(getattr(lib(), name)(x.data_ptr(), ldx, q_gate.data_ptr(), s_gate.data_ptr(),
                                 q_up.data_ptr(), s_up.data_ptr(), ldq, act, out.data_ptr(), ldh,
                                 g.data_ptr() if g is not None else None,
@@ -489,9 +499,7 @@ def gated_backward(dh, g, u, activation="silu", out=None):
     if _matrix(u, M, N, bf16, dev, "u") != ldgu:
         raise ValueError("g and u: expected one row stride")
     width = 2 * _round_up(N, 128)
-    if out is None:
-        out = torch.empty((M, width), dtype=bf16, device=dev)
-    ldo = _matrix(out, M, width, bf16, dev, "out")
+    out, ldo = _output(out, M, width, 8, bf16, dev)
     _check(lib().fp8blk_gated_backward(dh.data_ptr(), lddh, g.data_ptr(), u.data_ptr(), ldgu, act,
                                        out.data_ptr(), ldo, M, N, _stream()), "fp8blk_gated_backward")
     return out
@@ -516,12 +524,14 @@ def epilogue_backward(dy, z=None, activation="none", dz=None, bias_grad=True, wo
         ldz = _matrix(z, M, N, bf16, dev, "z")
     elif act != 0:
         raise ValueError("z: needed for every activation but none")
-    if dz is None:
-        dz = dy if act == 0 else _new(M, N, 8, bf16, dev)
-    lddz = _matrix(dz, M, N, bf16, dev, "dz")
-    dbias = torch.empty(N, dtype=torch.float32, device=dev) if bias_grad else None
-    need = epilogue_backward_workspace_size(M, N) if bias_grad else 0
-    workspace, ws, ws_len = _scratch(workspace, need, dev)
+    if dz is None and act == 0:
+        dz, lddz = dy, lddy
+    else:
+        dz, lddz = _output(dz, M, N, 8, bf16, dev, "dz")
+    dbias, ws, ws_len = None, None, 0
+    if bias_grad:
+        dbias = torch.empty(N, dtype=torch.float32, device=dev)
+        workspace, ws, ws_len = _scratch(workspace, epilogue_backward_workspace_size, (M, N), dev)
     _check(lib().fp8blk_epilogue_backward(dy.data_ptr(), lddy, z.data_ptr() if z is not None else None,
                                           ldz, act, dz.data_ptr(), lddz,
                                           dbias.data_ptr() if bias_grad else None, M, N, ws, ws_len,
@@ -543,11 +553,13 @@ def transpose_weight(q, scale_inv, qt=None, st=None):
     N, K = _dims(q, "q")
     dev = _device(q, "q")
     ldq = _weight(q, scale_inv, N, K, dev, "weight")
-    if qt is None:
-        qt = _new(K, N, 16, torch.uint8, dev)
     if st is None:
         st = torch.empty((_cdiv(K, 128), _cdiv(N, 128)), dtype=torch.float32, device=dev)
-    ldqt = _weight(qt, st, K, N, dev, "transposed weight")
+    if qt is None:
+        qt, ldqt = _new(K, N, 16, torch.uint8, dev)
+        _scales(st, K, N, dev, "transposed weight")
+    else:
+        ldqt = _weight(qt, st, K, N, dev, "transposed weight")
     _transpose_into(q, scale_inv, ldq, qt.data_ptr(), ldqt, st.data_ptr(), st.shape[1], 0)
     return qt, st
 
@@ -592,10 +604,8 @@ def linear_grad_weight(dz, x, out=None, accumulate=False, dtype=None, workspace=
         raise ValueError(f"dw: expected float32 or bfloat16, got {dtype}")
     if accumulate and (out is None or dtype != f32):
         raise ValueError("accumulate: needs a float32 out")
-    if out is None:
-        out = _new(N, K, 4 if dtype == f32 else 8, dtype, dev)
-    lddw = _matrix(out, N, K, dtype, dev, "out")
-    workspace, ws, ws_len = _scratch(workspace, linear_grad_weight_workspace_size(M, N, K), dev)
+    out, lddw = _output(out, N, K, 4 if dtype == f32 else 8, dtype, dev)
+    workspace, ws, ws_len = _scratch(workspace, linear_grad_weight_workspace_size, (M, N, K), dev)
     _check(lib().fp8blk_linear_grad_weight(dz.data_ptr(), lddz, x.data_ptr(), ldx, out.data_ptr(), lddw,
                                            int(dtype == f32), int(accumulate), M, N, K, ws, ws_len,
                                            _stream()), "fp8blk_linear_grad_weight")

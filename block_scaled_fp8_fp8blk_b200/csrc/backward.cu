@@ -176,6 +176,8 @@ struct RowSplit {
   int64_t rows, splits;
 };
 RowSplit row_split(int64_t M, int64_t N) {
+  // Few rows: one run, which needs no second kernel.
+  if (M <= 128) return {round_up(M, kRowsPerStep), 1};
   const int64_t strips = cdiv(N, kStripCols), want = cdiv(2368, strips);
   const int64_t rows = round_up(cdiv(M, want), kRowsPerStep);
   return {rows, cdiv(M, rows)};
