@@ -225,6 +225,87 @@ def test_linear_epilogue_parts(mode, M, name, parts):
 
 
 @pytest.mark.parametrize("mode", ["w8a16", "w8a8"])
+@pytest.mark.parametrize("M,K,N", [(4, 300, 137), (100, 700, 333), (260, 300, 137), (9000, 3000, 200)])
+def test_linear_epilogue_everything_at_once(mode, M, K, N):
+    """Bias, activation, kept z and the residual updated in place; the last size
+    walks two unequal raster groups."""
+    run_linear(mode, M, K, N, "gelu_tanh", bias=True, keep=True, in_place=True, seed=17)
+
+
+@pytest.mark.parametrize("mode", ["w8a16", "w8a8"])
+@pytest.mark.parametrize("M", [1, 50, 129, 300])
+def test_rows_behind_the_last_token_stay(mode, M):
+    """Buffers of more rows than tokens: what lies behind is not written."""
+    g = gen(18)
+    K, N = 256, 200
+    w, wu = weight(g, N, K), weight(g, N, K)
+    x, r = normal(g, M + 9, K)[:M], normal(g, M + 9, N)[:M]
+    big = [torch.full((M + 9, N), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(5)]
+    y, z, h, a, b = (t[:M] for t in big)
+    FUNCS["linear", mode](x, *w, residual=r, preact=z, out=y)
+    FUNCS["gated", mode](x, *w, *wu, preact=(a, b), out=h)
+    assert all((t[M:] == 7.0).all() and not (t[:M] == 7.0).all() for t in big)
+    dgu = torch.full((M + 9, 512), 7.0, dtype=torch.bfloat16, device=DEV)
+    fb.gated_backward(h, a, b, out=dgu[:M])
+    fb.epilogue_backward(h, z, activation="silu", dz=y)
+    assert (dgu[M:] == 7.0).all() and (big[0][M:] == 7.0).all()
+    dw = torch.full((N + 9, K), 7.0, device=DEV)
+    fb.linear_grad_weight(y, x, out=dw[:N])
+    qt = torch.full((K + 9, 208), 0xA5, dtype=torch.uint8, device=DEV)
+    fb.transpose_weight(*w, qt=qt[:K, :N])
+    assert (dw[N:] == 7.0).all() and (qt[K:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("mode", ["w8a16", "w8a8"])
+def test_offsets_beyond_32_bits(mode):
+    """Activations of more than 2^32 bytes (and 2^31 elements): rows at both ends."""
+    M, K, N = 70000, 64, 32768
+    g = gen(19)
+    w, wu = weight(g, N, K), weight(g, N, K)
+    x = normal(g, M, K)
+    rows_ = torch.cat([torch.arange(3), torch.arange(65500, 65560), torch.arange(M - 3, M)]).to(DEV)
+    y = torch.ones((M, N), dtype=torch.bfloat16, device=DEV)
+    FUNCS["linear", mode](x, *w, residual=y, out=y)
+    xd = activations(mode, x[rows_].contiguous())
+    zd, ud = xd @ dequantized(*w).T, xd @ dequantized(*wu).T
+    within(y[rows_], zd + 1, HALF * (zd + 1).abs() + 1e-4, "y")
+    kept = tuple(torch.empty((M, N), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    FUNCS["gated", mode](x, *w, *wu, activation="silu", preact=kept, out=y)
+    a, s = act("silu", zd)
+    within(y[rows_], a * ud, HALF * (a * ud).abs() + 1e-4, "h")
+    within(kept[1][rows_], ud, HALF * ud.abs() + 1e-4, "u")
+    dgu = fb.gated_backward(y, *kept)
+    d, gg, uu = (t[rows_].double() for t in (y, *kept))
+    a, s = act("silu", gg)
+    within(dgu[rows_, :N], d * uu * s, HALF * (d * uu * s).abs() + 1e-6, "dg")
+    within(dgu[rows_, N:], d * a, HALF * (d * a).abs() + 1e-6, "du")
+    dz, db = fb.epilogue_backward(y, kept[0], activation="silu", dz=y)
+    within(dz[rows_], d * s, HALF * (d * s).abs() + 1e-6, "dz")
+    dw = fb.linear_grad_weight(dz, x)
+    cols = [0, 1, N - 1]
+    want = dz[:, cols].double().T @ x.double()
+    within(dw[cols], want, (M / 8 + 16) * 2.0 ** -22 * (dz[:, cols].double().abs().T @ x.double().abs()), "dw")
+
+
+def test_weights_beyond_32_bits():
+    """Weight gradients and transposed codes of more than 2^31 elements."""
+    g = gen(20)
+    N, K = 70000, 32768
+    dz, x = normal(g, 16, N), normal(g, 16, K)
+    dw = fb.linear_grad_weight(dz, x)
+    sel = [0, 65536, N - 1]
+    want = dz[:, sel].double().T @ x.double()
+    within(dw[sel], want, 10 * 2.0 ** -22 * (dz[:, sel].double().abs().T @ x.double().abs()), "dw")
+    del dw
+    q = torch.arange(251, dtype=torch.uint8, device=DEV).repeat(N * K // 251 + 1)[:N * K].view(N, K)
+    s = torch.rand((-(-N // 128), K // 128), device=DEV)
+    qt, st = fb.transpose_weight(q, s)
+    for k in (0, 4097, K - 1):
+        assert torch.equal(qt[k], q[:, k])
+    assert torch.equal(st, s.t())
+
+
+@pytest.mark.parametrize("mode", ["w8a16", "w8a8"])
 @pytest.mark.parametrize("M", [1, 48, 128, 300])
 def test_empty_epilogue_is_the_linear(mode, M):
     """Without bias, activation and residual the result is the linear's, bit for bit."""
