@@ -63,20 +63,6 @@ struct GradCfg {
 };
 
 // ------------------------------------------------------- CTA-pair instructions
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
-}
-// The address, in the cluster's shared window, of the given CTA's copy of p.
-__device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
-  return a;
-}
 // Arrival on a barrier of the pair that says only that this warp's TMEM reads are
 // done (ordered by tcgen05.wait and the tcgen05 fences on both sides): no memory
 // is handed over, and a release at cluster scope, which waits for the warp's

@@ -53,6 +53,12 @@
 // meet in one thread and act(g) * u is stored from the staging buffer as a
 // plain y is: the pre-activations never leave the SM unless the caller keeps
 // them. The multiply work per slab is unchanged.
+//
+// SPLIT > 1 (with an epilogue only): when there are far fewer tiles than SMs (a
+// narrow layer and few tokens), a cluster of SPLIT CTAs shares one tile, each
+// taking a run of its K slabs; at the end the CTAs trade FP32 sums through
+// distributed shared memory, so that each has the whole sum, added in a fixed
+// order, of 1 / SPLIT of the tile's columns, and finishes those.
 #include <cuda_bf16.h>
 
 #include <cstring>
@@ -158,7 +164,132 @@ __device__ __forceinline__ const CUtensorMap* residual_map(const EpiParams<EPI>&
   return nullptr;
 }
 
-template <int EPI>
+// (In PTX, so that choosing among array elements stays a choice of registers and
+// does not become an index into memory.)
+__device__ __forceinline__ uint64_t select64(bool c, uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tselp.b64 %0, %1, %2, p;\n\t}"
+      : "=l"(r)
+      : "l"(a), "l"(b), "r"(static_cast<int>(c)));
+  return r;
+}
+
+// 16 columns of a row, of which the first `left` exist; p is 16-byte aligned.
+__device__ __forceinline__ void store_row16(uint16_t* p, const float (&f)[16], int left) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = cvt_bf16x2(f[2 * i + 1], f[2 * i]);
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    if (left >= 8 * g + 8) {
+      reinterpret_cast<uint4*>(p)[g] = make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+    } else {
+#pragma unroll
+      for (int i = 8 * g; i < 8 * g + 8; ++i)
+        if (i < left) p[i] = static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+    }
+  }
+}
+__device__ __forceinline__ void add_row16(const uint16_t* p, float (&f)[16], int left) {
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    if (left >= 8 * g + 8) {
+      const uint4 r = reinterpret_cast<const uint4*>(p)[g];
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[8 * g + 2 * i] += bf16_lo_to_f32(w[i]);
+        f[8 * g + 2 * i + 1] += bf16_hi_to_f32(w[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 8 * g; i < 8 * g + 8; ++i)
+        if (i < left) f[i] += bf16_bits_to_f32(p[i]);
+    }
+  }
+}
+
+// The end of a tile shared by a cluster of S CTAs. A part is 1 / S of the tile:
+// 128 / S column pairs (gated: half of them gate, half up, of the same outputs);
+// warp (quad, h) holds 32 rows of the S / 2 parts h S / 2 .., and CTA q finishes
+// part q. The other CTAs' sums of a part arrive in the stage ring (free once
+// every CTA has finished its slabs), one slot per CTA, [quad][pair][lane].
+// Every thread of the cluster passes both barriers, whatever happened before.
+template <int EPI, int S>
+__device__ __forceinline__ void finish_split(uint64_t (&acc)[64], bool ok, uint8_t* ring, int rank,
+                                             int quad, int h, int lane, int nt, int r0, int M,
+                                             int N, uint16_t* y, int64_t ldy,
+                                             const EpiParams<EPI>& ep) {
+  constexpr int PP = 128 / S, PL = S / 2, SLOT = PP * 1024;
+  constexpr bool GATED = EPI == kEpiGated;
+  auto at = [](int pl, int i) {  // index in acc of pair i of the warp's part pl
+    if (!GATED) return pl * PP + i;
+    return i < PP / 2 ? pl * (PP / 2) + i : 32 + pl * (PP / 2) + i - PP / 2;
+  };
+  const bool rows = r0 < M;  // the warp has rows
+  cluster_sync();
+  if (ok && rows) {
+#pragma unroll
+    for (int pl = 0; pl < PL; ++pl) {
+      const int q = h * PL + pl;
+      if (q != rank) {
+        const int slot = rank < q ? rank : rank - 1;
+        const uint32_t a = map_to_rank(ring, q) + slot * SLOT + quad * (PP * 256) + lane * 8;
+#pragma unroll
+        for (int i = 0; i < PP; ++i) st_cluster_u64(a + 256u * i, acc[at(pl, i)]);
+      }
+    }
+  }
+  cluster_sync();
+  if (!ok || !rows || h != rank / PL) return;
+  uint64_t v[PP];
+#pragma unroll
+  for (int i = 0; i < PP; ++i) {
+    v[i] = acc[at(0, i)];
+#pragma unroll
+    for (int pl = 1; pl < PL; ++pl) v[i] = select64(pl == rank % PL, acc[at(pl, i)], v[i]);
+  }
+  const uint8_t* in = ring + quad * (PP * 256) + lane * 8;
+#pragma unroll 1
+  for (int s = 0; s < S - 1; ++s) {
+#pragma unroll
+    for (int i = 0; i < PP; ++i)
+      fadd2(v[i], *reinterpret_cast<const uint64_t*>(in + s * SLOT + 256 * i));
+  }
+  const int m = r0 + lane;
+  if (m >= M) return;
+  constexpr int COLS = GATED ? PP : 2 * PP;  // output columns of a part
+  const int col0 = (nt * S + rank) * COLS;
+  const int64_t row = m;
+#pragma unroll
+  for (int c = 0; c < COLS / 16; ++c) {
+    const int base = col0 + 16 * c, left = N - base;
+    if (left <= 0) break;
+    float f[16];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) unpack2(v[8 * c + p], f[2 * p], f[2 * p + 1]);
+    if constexpr (GATED) {
+      float u[16];
+#pragma unroll
+      for (int p = 0; p < 8; ++p) unpack2(v[PP / 2 + 8 * c + p], u[2 * p], u[2 * p + 1]);
+      if (ep.e.g) {
+        store_row16(ep.e.g + row * ep.e.ldgu + base, f, left);
+        store_row16(ep.e.u + row * ep.e.ldgu + base, u, left);
+      }
+      act_apply(ep.e.act, f);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) f[i] *= u[i];
+    } else {
+      if (ep.e.bias) add_row16(ep.e.bias + base, f, left);
+      if (ep.e.preact) store_row16(ep.e.preact + row * ep.e.ldp + base, f, left);
+      act_apply(ep.e.act, f);
+      if (ep.e.residual) add_row16(ep.e.residual + row * ep.e.ldr + base, f, left);
+    }
+    store_row16(y + row * ldy + base, f, left);
+  }
+}
+
+template <int EPI, int SPLIT>
 __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
     w8a8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_y, const float* __restrict__ sx,
@@ -169,6 +300,7 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
   using C = W8A8Cfg;
   constexpr bool GATED = EPI == kEpiGated;
   constexpr int TILE_N = GATED ? C::BN / 2 : C::BN;  // output columns of a tile
+  static_assert(SPLIT == 1 || EPI != kEpiPlain, "only with an epilogue");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;                            // ST stages: A then B
@@ -184,7 +316,11 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
   const int ntiles_n = ntiles_total / mtiles;
   const int my_tiles =
       static_cast<int>(blockIdx.x) < ntiles_total ? (ntiles_total - 1 - blockIdx.x) / gridDim.x + 1 : 0;
-  const int total_slabs = my_tiles * KB;
+  // This CTA's run of a tile's slabs, and its tiles.
+  const int rank = SPLIT > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int kb0 = SPLIT > 1 ? KB * rank / SPLIT : 0, kb1 = SPLIT > 1 ? KB * (rank + 1) / SPLIT : KB;
+  const int first_tile = static_cast<int>(blockIdx.x) / SPLIT;
+  const int total_slabs = SPLIT > 1 ? kb1 - kb0 : my_tiles * KB;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::ST; ++s) mbar_init(&full[s], GATED ? 3 : 2);
@@ -230,11 +366,11 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
       if (is_a) pdl_wait();
       int j = 0;  // slab counter (across tiles)
       bool ok = true;
-      for (int tile = blockIdx.x; tile < ntiles_total && ok; tile += gridDim.x) {
+      for (int tile = first_tile; tile < ntiles_total && ok; tile += gridDim.x) {
         int mt, nt;
         tile_coords(tile, mtiles, ntiles_n, gm, mt, nt);
         const int row0 = is_a ? mt * C::BM : nt * TILE_N;
-        for (int kb = 0; kb < KB; ++kb, ++j) {
+        for (int kb = kb0; kb < kb1; ++kb, ++j) {
           const int stage = j & (C::ST - 1);
           if (j >= C::ST) {  // the slab that last used this stage has finished
             const int jo = j - C::ST;
@@ -274,6 +410,11 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
       // Drain: this issuer's MMAs have completed before TMEM is released.
       if (last >= 0) wait_use(&done[last & (C::RD - 1)], last / C::RD, err, kErrWaitMma);
     }
+    if constexpr (SPLIT > 1) {  // the barriers of finish_split
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     setmaxnreg_inc<C::REG_EPI>();
     // -------------------------------------------------- promotion/epilogue
@@ -301,7 +442,7 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
         tma_load_2d(stage, residual_map(ep), &rfull[ew], base, r0);
       }
     };
-    for (int tile = blockIdx.x; tile < ntiles_total && ok; tile += gridDim.x) {
+    for (int tile = first_tile; tile < ntiles_total && ok; tile += gridDim.x) {
       int mt, nt;
       tile_coords(tile, mtiles, ntiles_n, gm, mt, nt);
       const int m0 = mt * C::BM;
@@ -317,7 +458,7 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
       uint64_t acc[64];  // column pairs (gated: 32 of the gate, then 32 of up)
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-      if constexpr (EPI == kEpiFused) {
+      if constexpr (EPI == kEpiFused && SPLIT == 1) {
         if (ep.e.residual && m0 + quad * 32 < M) {
           // (The staging buffer serves z first where that is kept.)
           if (!ep.e.preact) load_residual(col0, m0 + quad * 32);
@@ -337,12 +478,12 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
       }
       // The two scale factors of a slab are loaded one slab ahead and only
       // multiplied when used, so the product does not wait on the loads.
-      float fx = has_cols ? __ldg(sx_col) : 0.0f, fw = has_cols ? __ldg(sw_row) : 0.0f;
-      float fu = GATED && has_cols ? __ldg(sw_up) : 0.0f;
-      for (int kb = 0; kb < KB; ++kb, ++j) {
+      float fx = has_cols ? __ldg(sx_col + kb0 * ldsx) : 0.0f, fw = has_cols ? __ldg(sw_row + kb0) : 0.0f;
+      float fu = GATED && has_cols ? __ldg(sw_up + kb0) : 0.0f;
+      for (int kb = kb0; kb < kb1; ++kb, ++j) {
         const float c = fx * fw;
         const float cu = GATED ? fx * fu : 0.0f;
-        if (has_cols && kb + 1 < KB) {
+        if (has_cols && kb + 1 < kb1) {
           fx = __ldg(sx_col + (kb + 1) * ldsx);
           fw = __ldg(sw_row + kb + 1);
           if constexpr (GATED) fu = __ldg(sw_up + kb + 1);
@@ -370,6 +511,10 @@ __global__ void __launch_bounds__(W8A8Cfg::THREADS, 1)
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pempty[j & 1]);
+      }
+      if constexpr (SPLIT > 1) {
+        finish_split<EPI, SPLIT>(acc, ok, smem, rank, quad, h, lane, nt, m0 + quad * 32, M, N, y, ldy, ep);
+        break;
       }
       if (!ok) break;
       // Output, 64 columns at a time: the staging buffer's previous store has
@@ -484,7 +629,7 @@ bool block_map(CUtensorMap* map, const uint16_t* p, int64_t n_tma, int64_t M, in
   return true;
 }
 
-template <int EPI>
+template <int EPI, int SPLIT = 1>
 cudaError_t launch_epi(const Launch& L, const uint8_t* qx, int64_t ldqx, const float* sx,
                        int64_t ldsx, const uint8_t* q, int64_t ldq, const float* sw, uint16_t* y,
                        int64_t ldy, int64_t M, int64_t N, int64_t K, bool after_act_quant,
@@ -513,7 +658,7 @@ cudaError_t launch_epi(const Launch& L, const uint8_t* qx, int64_t ldqx, const f
         !block_map(&ep.tm_u, ep.e.u, n_tma, M, ep.e.ldgu))
       return cudaErrorInvalidValue;
   }
-  auto kern = w8a8_gemm_kernel<EPI>;
+  auto kern = w8a8_gemm_kernel<EPI, SPLIT>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   {
@@ -530,7 +675,8 @@ cudaError_t launch_epi(const Launch& L, const uint8_t* qx, int64_t ldqx, const f
   const int64_t mtiles = cdiv(M, C::BM), tiles = mtiles * cdiv(N, kTileN);
   // Slab counters are 32-bit per CTA.
   if (tiles * cdiv(K, 128) > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
-  const int grid = static_cast<int>(tiles < L.num_sms ? tiles : L.num_sms);
+  const int grid = SPLIT > 1 ? static_cast<int>(tiles * SPLIT)
+                             : static_cast<int>(tiles < L.num_sms ? tiles : L.num_sms);
   // After the activation quantizer: a programmatic dependent launch, so the
   // GEMM's set-up and weight loads overlap that kernel.
   cudaLaunchConfig_t cfg = {};
@@ -538,16 +684,91 @@ cudaError_t launch_epi(const Launch& L, const uint8_t* qx, int64_t ldqx, const f
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = L.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  int nattr = 0;
+  if (after_act_quant) {
+    attr[nattr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[nattr++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (SPLIT > 1) {
+    attr[nattr].id = cudaLaunchAttributeClusterDimension;
+    attr[nattr].val.clusterDim.x = SPLIT;
+    attr[nattr].val.clusterDim.y = 1;
+    attr[nattr++].val.clusterDim.z = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = after_act_quant ? 1 : 0;
+  cfg.numAttrs = nattr;
   return cudaLaunchKernelEx(&cfg, kern, ta, tb, ty, sx, ldsx, sw, y, ldy, static_cast<int>(M),
                             static_cast<int>(N), static_cast<int>(n_tma),
                             static_cast<int>(cdiv(K, 128)), static_cast<int>(mtiles),
                             static_cast<int>(tiles), raster_group(mtiles, C::BM * K, kRasterBytesW8A8),
                             static_cast<int>(a_rows * 128), L.err, ep);
+}
+
+// Clusters of S CTAs that can be resident at once (0 on an error; queried once per
+// device and form): a cluster lies within one group of SMs, so it is fewer than
+// num_sms / S.
+template <int EPI, int S>
+int64_t resident_clusters() {
+  static int known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = __atomic_load_n(&known[dev], __ATOMIC_RELAXED);
+  if (n == 0) {
+    auto kern = w8a8_gemm_kernel<EPI, S>;
+    if (ensure_smem_limit(reinterpret_cast<const void*>(kern), W8A8Cfg::SMEM) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(S);
+    cfg.blockDim = dim3(W8A8Cfg::THREADS);
+    cfg.dynamicSmemBytes = W8A8Cfg::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+    __atomic_store_n(&known[dev], n, __ATOMIC_RELAXED);
+  }
+  return n;
+}
+
+// CTAs per tile: the least of rounds x (slabs per CTA + what a round costs
+// besides), in slabs (0.5 us each here): a start and an end of about kRoundSlabs,
+// and for the trade kTradeSlabs, more with two CTAs, where each finishes half of
+// a tile. At least kMinSplitSlabs slabs each. Measured (one CTA per tile -> this rule,
+// 16 tokens, residual): 25600 -> 5120 121 -> 47 us, 8192 -> 5120
+// 49 -> 25, 4096 -> 2560 33 -> 16, 8192 -> 16384 51 -> 45, 1024 -> 5120 18 -> 16.
+constexpr int64_t kRoundSlabs = 8, kTradeSlabs = 4, kTradeSlabs2 = 16, kMinSplitSlabs = 2;
+template <int EPI>
+int split_of(int64_t tiles, int64_t KB, int num_sms) {
+  int best = 1;
+  int64_t cost = cdiv(tiles, num_sms) * (KB + kRoundSlabs);
+  if (tiles * 2 > num_sms || KB < 2 * kMinSplitSlabs) return 1;  // not few, or nothing to share
+  auto consider = [&](int s, int64_t resident, int64_t trade) {
+    if (resident <= 0 || KB < s * kMinSplitSlabs) return;
+    const int64_t c = cdiv(tiles, resident) * (cdiv(KB, s) + kRoundSlabs + trade);
+    if (c < cost) cost = c, best = s;
+  };
+  consider(2, resident_clusters<EPI, 2>(), kTradeSlabs2);
+  consider(4, resident_clusters<EPI, 4>(), kTradeSlabs);
+  consider(8, resident_clusters<EPI, 8>(), kTradeSlabs);
+  return best;
+}
+
+template <int EPI>
+cudaError_t launch_split(const Launch& L, const uint8_t* qx, int64_t ldqx, const float* sx,
+                         int64_t ldsx, const uint8_t* q, int64_t ldq, const float* sw, uint16_t* y,
+                         int64_t ldy, int64_t M, int64_t N, int64_t K, EpiParams<EPI>& ep) {
+  using C = W8A8Cfg;
+  const int64_t tiles = cdiv(M, C::BM) * cdiv(N, EPI == kEpiGated ? C::BN / 2 : C::BN);
+  switch (split_of<EPI>(tiles, cdiv(K, 128), L.num_sms)) {
+    case 8: return launch_epi<EPI, 8>(L, qx, ldqx, sx, ldsx, q, ldq, sw, y, ldy, M, N, K, true, ep);
+    case 4: return launch_epi<EPI, 4>(L, qx, ldqx, sx, ldsx, q, ldq, sw, y, ldy, M, N, K, true, ep);
+    case 2: return launch_epi<EPI, 2>(L, qx, ldqx, sx, ldsx, q, ldq, sw, y, ldy, M, N, K, true, ep);
+  }
+  return launch_epi<EPI>(L, qx, ldqx, sx, ldsx, q, ldq, sw, y, ldy, M, N, K, true, ep);
 }
 
 }  // namespace
@@ -566,7 +787,7 @@ cudaError_t launch_w8a8_fused(const Launch& L, const uint8_t* qx, int64_t ldqx, 
                               const FusedEpi& e) {
   EpiParams<kEpiFused> ep;
   ep.e = e;
-  return launch_epi<kEpiFused>(L, qx, ldqx, sx, ldsx, q, ldq, sw, y, ldy, M, N, K, true, ep);
+  return launch_split<kEpiFused>(L, qx, ldqx, sx, ldsx, q, ldq, sw, y, ldy, M, N, K, ep);
 }
 
 cudaError_t launch_w8a8_gated(const Launch& L, const uint8_t* qx, int64_t ldqx, const float* sx,
@@ -575,7 +796,7 @@ cudaError_t launch_w8a8_gated(const Launch& L, const uint8_t* qx, int64_t ldqx, 
                               const GatedEpi& e) {
   EpiParams<kEpiGated> ep;
   ep.e = e;
-  return launch_epi<kEpiGated>(L, qx, ldqx, sx, ldsx, q, ldq, sw, h, ldh, M, N, K, true, ep);
+  return launch_split<kEpiGated>(L, qx, ldqx, sx, ldsx, q, ldq, sw, h, ldh, M, N, K, ep);
 }
 
 }  // namespace fp8blk

@@ -138,6 +138,26 @@ struct Ring {
 // Parity of the most recent phase of a ring slot that was used `uses` times.
 __device__ __forceinline__ uint32_t last_parity(int uses) { return static_cast<uint32_t>((uses - 1) & 1); }
 
+// ------------------------------------------------------- thread-block clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of every CTA of the cluster (release on arrival, acquire after).
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
+}
+// The address, in the cluster's shared window, of the given CTA's copy of p.
+__device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
+  asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
 // ----------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -432,6 +452,11 @@ __device__ __forceinline__ uint64_t pack_u32x2(uint32_t lo, uint32_t hi) {
 // acc = p * c + acc on two FP32 lanes at once (each lane one rounded FMA).
 __device__ __forceinline__ void ffma2(uint64_t& acc, uint64_t p, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(p), "l"(c));
+}
+
+// a += b on two FP32 lanes at once.
+__device__ __forceinline__ void fadd2(uint64_t& a, uint64_t b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
 }
 
 // acc2[j] += (TMEM[lane, t + 2j], TMEM[lane, t + 2j + 1]) * (c, c) for

@@ -337,7 +337,9 @@ typedef struct fp8blk_epilogue {
 /* ---------------------------------------------------------------------------
  * fp8blk_linear_w8a16 / fp8blk_linear_w8a8 with an epilogue. Arguments,
  * workspace and ordering as for those calls; K = 0 gives y = act(bias) +
- * residual. The FP32 sum is never rounded before the epilogue.
+ * residual. The FP32 sum is never rounded before the epilogue. The order of a sum
+ * depends on the sizes and the GPU alone (repeated calls agree bit for bit), but
+ * it may differ from that of the linear without epilogue.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, WORKSPACE, CUDA.
  * ------------------------------------------------------------------------- */
 FP8BLK_EXPORT fp8blk_status fp8blk_linear_w8a16_epilogue(

@@ -232,6 +232,21 @@ def test_linear_epilogue_everything_at_once(mode, M, K, N):
     run_linear(mode, M, K, N, "gelu_tanh", bias=True, keep=True, in_place=True, seed=17)
 
 
+# Few tiles and many K slabs: W8A8 shares a tile among 2, 4 or 8 SMs.
+SPLIT_SHAPES = [(1, 8192, 640), (40, 8192, 256), (128, 2560, 5120), (100, 4100, 2570), (300, 2100, 1000),
+                (129, 16000, 130), (1, 25600, 5120), (256, 2048, 9000)]
+
+
+@pytest.mark.parametrize("M,K,N", SPLIT_SHAPES)
+def test_few_tiles_and_many_slabs(M, K, N):
+    run_linear("w8a8", M, K, N, "silu", bias=True, keep=True, in_place=True, seed=K)
+    run_linear("w8a8", M, K, N, residual=True, seed=K + 1)
+    run_gated("w8a8", M, K, N // 2, "gelu", keep=True, seed=K + 2)
+    x, w, first = run_linear("w8a8", M, K, N, "gelu", seed=K + 3)
+    for _ in range(3):
+        assert same_bits(fb.linear_w8a8_epilogue(x, *w, activation="gelu"), first)
+
+
 @pytest.mark.parametrize("mode", ["w8a16", "w8a8"])
 @pytest.mark.parametrize("M", [1, 50, 129, 300])
 def test_rows_behind_the_last_token_stay(mode, M):
