@@ -146,16 +146,21 @@ def _stream():
 def _ld(t) -> int:
     if t.dim() != 2:
         raise ValueError("expected a 2-D tensor")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError("expected unit column stride")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+    if ld >= cols:
+        return ld or 1
+    if rows > 1:
         raise ValueError("rows overlap: expected a row stride of at least the columns")
-    return max(t.shape[1], t.stride(0), 1)
+    return cols or 1
 
 
 def _padded(rows: int, cols: int, ld: int, dtype, device):
     import torch
-    return torch.empty((rows, ld), dtype=dtype, device=device)[:, :cols]
+    buf = torch.empty((rows, ld), dtype=dtype, device=device)
+    return buf if ld == cols else buf[:, :cols]
 
 
 def version() -> int:
@@ -210,9 +215,10 @@ def _linear(mode: int, name: str, x, q, scale_inv, out, workspace):
         raise ValueError("x and q disagree on K")
     if out is None:
         out = _padded(M, N, _round_up(max(N, 1), 8), torch.bfloat16, x.device)
-    need = workspace_size(mode, M, N, K)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    if workspace is None:
+        need = workspace_size(mode, M, N, K)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_len = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(getattr(lib(), name)(x.data_ptr(), _ld(x), q.data_ptr(), _ld(q), scale_inv.data_ptr(),
