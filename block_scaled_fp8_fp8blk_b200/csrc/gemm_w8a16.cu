@@ -152,16 +152,23 @@ __device__ __forceinline__ uint32_t ring_parity(int item, int depth) {
 // and last stream-K segments can be partial. dp_tiles = 0 is pure stream-K,
 // dp_tiles = tiles pure round robin.
 // (Slab counts fit in 32 bits: the host checks tiles x KB.)
+// FEW: U may be smaller than G (with one sub-tile the host launches at most U CTAs).
+template <bool FEW>
 struct Schedule {
   int u, end, first;
   int tile, KB, dp_tiles;
   __device__ Schedule(int kb_per_tile, int tiles, int dp)
       : tile(static_cast<int>(blockIdx.x)), KB(kb_per_tile), dp_tiles(dp) {
     const int64_t U = static_cast<int64_t>(tiles - dp) * kb_per_tile;
-    const int64_t S = U < gridDim.x ? U : gridDim.x;
-    const bool some = blockIdx.x < S;
-    first = u = some ? static_cast<int>(U * blockIdx.x / S) : 0;
-    end = some ? static_cast<int>(U * (blockIdx.x + 1) / S) : 0;
+    if constexpr (FEW) {
+      const int64_t S = U < gridDim.x ? U : gridDim.x;
+      const bool some = blockIdx.x < S;
+      first = u = some ? static_cast<int>(U * blockIdx.x / S) : 0;
+      end = some ? static_cast<int>(U * (blockIdx.x + 1) / S) : 0;
+    } else {
+      first = u = static_cast<int>(U * blockIdx.x / gridDim.x);
+      end = static_cast<int>(U * (blockIdx.x + 1) / gridDim.x);
+    }
   }
   __device__ int slabs() const {
     const int dp = tile < dp_tiles ? ((dp_tiles - 1 - tile) / static_cast<int>(gridDim.x) + 1) * KB : 0;
@@ -260,14 +267,14 @@ __device__ __forceinline__ void tile_of(int t, int mtiles, int ntiles_total, int
 // ------------------------------------------------------------------- output
 // Plain: 16 tokens x 32 columns staged as rows of 32 BF16, then each lane
 // stores 16 contiguous values (32 bytes) of one row of y.
-__device__ __forceinline__ void stage_and_flush(uint8_t* stg, const float (&v)[16], uint16_t* y,
+__device__ __forceinline__ void stage_and_flush(uint8_t* stg, const uint64_t* acc, uint16_t* y,
                                                 int64_t ldy, int m0, int c_first, int M, int N,
                                                 int lane) {
 #pragma unroll
-  for (int e = 0; e < 16; e += 2) {
-    const uint32_t b2 = cvt_bf16x2(v[e + 1], v[e]);
-    *reinterpret_cast<uint16_t*>(stg + e * 64 + lane * 2) = static_cast<uint16_t>(b2 & 0xFFFFu);
-    *reinterpret_cast<uint16_t*>(stg + (e + 1) * 64 + lane * 2) = static_cast<uint16_t>(b2 >> 16);
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b2 = cvt_bf16x2_pair(acc[e]);
+    *reinterpret_cast<uint16_t*>(stg + (2 * e) * 64 + lane * 2) = static_cast<uint16_t>(b2 & 0xFFFFu);
+    *reinterpret_cast<uint16_t*>(stg + (2 * e + 1) * 64 + lane * 2) = static_cast<uint16_t>(b2 >> 16);
   }
   __syncwarp();
   const int rr = lane >> 1, hh = lane & 1;
@@ -448,7 +455,8 @@ __global__ void __launch_bounds__(512, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pempty + C::PB * 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int total_slabs = Schedule(KB, ntiles_total, dp_tiles).slabs();
+  using Sched = Schedule<NSUB == 2>;
+  const int total_slabs = Sched(KB, ntiles_total, dp_tiles).slabs();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::QS; ++s) {
@@ -497,7 +505,7 @@ __global__ void __launch_bounds__(512, 1)
       if (!early_weights) pdl_wait();
       int j = 0;  // slab counter (across tiles)
       bool ok = true;
-      Schedule sc(KB, ntiles_total, dp_tiles);
+      Sched sc(KB, ntiles_total, dp_tiles);
       int tile, kb0, kb1;
       while (ok && sc.next(tile, kb0, kb1)) {
         int mt, nt;
@@ -522,7 +530,7 @@ __global__ void __launch_bounds__(512, 1)
       pdl_wait();
       int i = 0;  // item counter (across tiles)
       bool ok = true;
-      Schedule sc(KB, ntiles_total, dp_tiles);
+      Sched sc(KB, ntiles_total, dp_tiles);
       int tile, kb0, kb1;
       while (ok && sc.next(tile, kb0, kb1)) {
         int mt, nt;
@@ -610,16 +618,15 @@ __global__ void __launch_bounds__(512, 1)
       int j = 0;
       bool ok = true;
       bool first_sk = true;  // the next stream-K segment is this CTA's first
-      Schedule sc(KB, ntiles_total, dp_tiles);
+      Sched sc(KB, ntiles_total, dp_tiles);
       int tile, kb0, kb1;
       while (ok && sc.next(tile, kb0, kb1)) {
         int mt, nt;
         tile_of<GROUPED>(tile, mtiles, ntiles_total, gm, mt, nt);
         const int m0 = mt * (BT * NSUB), n0 = nt * TILE_N;
         const float* sw_row = sw_of_lane + static_cast<int64_t>(n0 >> 7) * KB;
-        const int nw = n0 + quad * (TILE_N / 4);  // first column of this warp
         if constexpr (EPI == kEpiFused) {
-          if (kb0 == 0 && kb1 == KB) fused_fetch(ft, ep.e, 0, m0 + 64 * h, nw, M, N, lane);
+          if (kb0 == 0 && kb1 == KB) fused_fetch(ft, ep.e, 0, m0 + 64 * h, n0 + quad * 32, M, N, lane);
         }
         uint64_t acc[64];  // acc[32t + p]: tokens 128t + 64h + 2p and 2p + 1
 #pragma unroll
@@ -676,6 +683,7 @@ __global__ void __launch_bounds__(512, 1)
         }
         // Output: sixteen tokens at a time through shared memory as rows of
         // 32 BF16 (this warp's columns of y), then 32-byte stores per lane.
+        const int nw = n0 + quad * (TILE_N / 4);  // first column of this warp
         uint16_t* yo = reinterpret_cast<uint16_t*>(y);
         auto first_token = [&](int i) { return m0 + 128 * (i >> 2) + 64 * h + 16 * (i & 3); };
         if constexpr (EPI == kEpiFused) {
@@ -690,11 +698,8 @@ __global__ void __launch_bounds__(512, 1)
           });
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float v[16];
-            group_values(acc + 8 * i, v);
-            stage_and_flush(stg, v, yo, ldy, first_token(i), nw, M, N, lane);
-          }
+          for (int i = 0; i < 8; ++i)
+            stage_and_flush(stg, acc + 8 * i, yo, ldy, first_token(i), nw, M, N, lane);
         }
       }
     } else if (((warp - 8) >> 2) < NSUB) {
@@ -711,7 +716,7 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + C::TMEM_P;
       int j = 0;
       bool ok = true;
-      Schedule sc(KB, ntiles_total, dp_tiles);
+      Sched sc(KB, ntiles_total, dp_tiles);
       int tile, kb0, kb1;
       bool first_segment = true;
       while (ok && sc.next(tile, kb0, kb1)) {
@@ -719,10 +724,8 @@ __global__ void __launch_bounds__(512, 1)
         tile_of<GROUPED>(tile, mtiles, ntiles_total, gm, tm, tn);
         const int m0 = tm * (BT * NSUB), n0 = tn * TILE_N;
         const float* sw_row = sw_of_lane + static_cast<int64_t>(n0 >> 7) * KB;
-        const int mt = m0 + t * BT;
-        const int nw = n0 + quad * (TILE_N / 4);  // first column of this warp
         if constexpr (EPI == kEpiFused) {
-          if (kb0 == 0 && kb1 == KB) fused_fetch(ft, ep.e, 0, mt, nw, M, N, lane);
+          if (kb0 == 0 && kb1 == KB) fused_fetch(ft, ep.e, 0, m0 + t * BT, n0 + quad * 32, M, N, lane);
         }
         uint64_t acc[BT / 2];
 #pragma unroll
@@ -780,6 +783,8 @@ __global__ void __launch_bounds__(512, 1)
         // weight row (column of y) per lane. Sixteen tokens at a time go
         // through shared memory as rows of 32 BF16, so that each lane then
         // stores 16 contiguous values (32 bytes) of one row of y.
+        const int mt = m0 + t * BT;
+        const int nw = n0 + quad * (TILE_N / 4);  // first column of this warp
         uint16_t* yo = reinterpret_cast<uint16_t*>(y);
         if constexpr (EPI == kEpiFused) {
           ft.bias = ep.e.bias && nw + lane < N ? bf16_bits_to_f32(__ldg(ep.e.bias + nw + lane)) : 0.0f;
@@ -793,11 +798,8 @@ __global__ void __launch_bounds__(512, 1)
           });
         } else {
 #pragma unroll
-          for (int i = 0; i < BT / 16; ++i) {
-            float v[16];
-            group_values(acc + 8 * i, v);
-            stage_and_flush(stg, v, yo, ldy, mt + 16 * i, nw, M, N, lane);
-          }
+          for (int i = 0; i < BT / 16; ++i)
+            stage_and_flush(stg, acc + 8 * i, yo, ldy, mt + 16 * i, nw, M, N, lane);
         }
       }
     } else {
