@@ -936,6 +936,13 @@ size_t streamk_bytes(int64_t grid, int tok) {
   return static_cast<size_t>(grid) * 2 * tok * 128 * sizeof(float);
 }
 
+// What the stream-K fix-up costs a call, in slabs of one CTA's time (a slab takes
+// about twice as long with 128 tokens). Measured, split -> whole, one token: 512
+// inputs and 5120 outputs (4 slabs in sequence against 2) 16.4 -> 12.3 us, 1024 and 10240
+// (8 against 5) 18.4 -> 14.4, 2048 and 256 (16 against 1) 14.3 -> 16.4; 128 tokens: 512 and
+// 5120 20.5 -> 16.4, 1024 and 256 (8 against 1) 16.4 -> 18.4.
+constexpr int64_t fixup_slabs(int bt) { return bt >= 128 ? 5 : 11; }
+
 template <int BT, int NSUB, bool GROUPED, int EPI>
 cudaError_t launch_bt(const Launch& L, const uint16_t* x, int64_t ldx, const uint8_t* q,
                       int64_t ldq, const float* sw, uint16_t* y, int64_t ldy, int64_t M,
@@ -980,6 +987,12 @@ cudaError_t launch_bt(const Launch& L, const uint16_t* x, int64_t ldx, const uin
     // streams the same share of the weights however few tiles there are.
     dp_tiles = 0;
     grid = tiles * KB < G ? tiles * KB : G;
+    if (EPI != kEpiPlain && cdiv(tiles, G) * KB <= cdiv(tiles * KB, G) + fixup_slabs(BT)) {
+      // Whole tiles where the even split would save less than its fix-up costs.
+      // (The plain linear keeps its order of sums.)
+      dp_tiles = tiles;
+      grid = tiles < G ? tiles : G;
+    }
     if (!ws || ws_bytes < streamk_bytes(grid, TOK)) return cudaErrorInvalidValue;
   } else {
     // Whole tiles round robin. When the last wave of tiles would leave at

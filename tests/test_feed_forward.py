@@ -323,10 +323,16 @@ def test_weights_beyond_32_bits():
 @pytest.mark.parametrize("mode", ["w8a16", "w8a8"])
 @pytest.mark.parametrize("M", [1, 48, 128, 300])
 def test_empty_epilogue_is_the_linear(mode, M):
-    """Without bias, activation and residual the result is the linear's, bit for bit."""
+    """Without bias, activation and residual the result is the linear's: bit for
+    bit where the slabs are added in the same order (always at these sizes,
+    but for W8A16 up to 128 tokens, where the plain call splits the tiles that
+    this one runs whole), else the same sum in another order, rounded."""
     x, w, y = run_linear(mode, M, 640, 1000)
-    plain = fb.linear_w8a16 if mode == "w8a16" else fb.linear_w8a8
-    assert same_bits(y, plain(x, *w))
+    plain = (fb.linear_w8a16 if mode == "w8a16" else fb.linear_w8a8)(x, *w)
+    if mode == "w8a8" or M > 128:
+        assert same_bits(y, plain)
+    xd, wd = activations(mode, x), dequantized(*w)
+    within(y, plain.double(), 2 * HALF * plain.double().abs() + 2 * acc(640) * (xd.abs() @ wd.abs().T), "order")
 
 
 @pytest.mark.parametrize("mode", ["w8a16", "w8a8"])
