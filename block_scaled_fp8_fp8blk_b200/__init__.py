@@ -89,6 +89,7 @@ EXPORTS = {
     "fp8blk_epilogue_backward": (_st, [_p, _i64, _p, _i64, _i32, _p, _i64, _p, _i64, _i64, _p, _sz, _p]),
     "fp8blk_epilogue_backward_workspace_size": (_sz, [_i64, _i64]),
     "fp8blk_transpose_weight": (_st, [_p, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _i32, _p]),
+    "fp8blk_transpose_gated_weights": (_st, [_p, _p, _p, _p, _i64, _i64, _i64, _p, _i64, _p, _p]),
     "fp8blk_linear_grad_weight": (_st, [_p, _i64, _p, _i64, _p, _i64, _i32, _i32, _i64, _i64, _i64, _p,
                                         _sz, _p]),
     "fp8blk_linear_grad_weight_workspace_size": (_sz, [_i64, _i64, _i64]),
@@ -545,13 +546,6 @@ def epilogue_backward(dy, z=None, activation="none", dz=None, bias_grad=True, wo
     return dz, dbias
 
 
-def _transpose_into(q, s, ldq, qt, ldqt, st, ldst, zero_pad):
-    """qt and st as addresses."""
-    N, K = q.shape
-    _check(lib().fp8blk_transpose_weight(q.data_ptr(), ldq, s.data_ptr(), N, K, qt, ldqt, st, ldst,
-                                         zero_pad, _stream()), "fp8blk_transpose_weight")
-
-
 def transpose_weight(q, scale_inv, qt=None, st=None):
     """(qt, st): the transposed block-FP8 weight, codes [K, N] and scales
     [ceil(K/128), ceil(N/128)], exact. dx = linear_w8a16(dz, qt, st)."""
@@ -566,7 +560,9 @@ def transpose_weight(q, scale_inv, qt=None, st=None):
         _scales(st, K, N, dev, "transposed weight")
     else:
         ldqt = _weight(qt, st, K, N, dev, "transposed weight")
-    _transpose_into(q, scale_inv, ldq, qt.data_ptr(), ldqt, st.data_ptr(), st.shape[1], 0)
+    _check(lib().fp8blk_transpose_weight(q.data_ptr(), ldq, scale_inv.data_ptr(), N, K, qt.data_ptr(),
+                                         ldqt, st.data_ptr(), st.shape[1], 0, _stream()),
+           "fp8blk_transpose_weight")
     return qt, st
 
 
@@ -577,7 +573,9 @@ def transpose_gated_weights(q_gate, s_gate, q_up, s_up, qt=None, st=None):
     import torch
     N, K = _dims(q_gate, "q_gate")
     dev = _device(q_gate, "q_gate")
-    ldq = (_weight(q_gate, s_gate, N, K, dev, "gate weight"), _weight(q_up, s_up, N, K, dev, "up weight"))
+    ldq = _weight(q_gate, s_gate, N, K, dev, "gate weight")
+    if _weight(q_up, s_up, N, K, dev, "up weight") != ldq:
+        raise ValueError("q_gate and q_up: expected one row stride")
     NB = _cdiv(N, 128)
     Np = 128 * NB
     if qt is None:
@@ -585,8 +583,10 @@ def transpose_gated_weights(q_gate, s_gate, q_up, s_up, qt=None, st=None):
     if st is None:
         st = torch.empty((_cdiv(K, 128), 2 * NB), dtype=torch.float32, device=dev)
     ldqt = _weight(qt, st, K, 2 * Np, dev, "transposed weight")
-    for i, (q, s) in enumerate(((q_gate, s_gate), (q_up, s_up))):
-        _transpose_into(q, s, ldq[i], qt.data_ptr() + i * Np, ldqt, st.data_ptr() + 4 * i * NB, 2 * NB, 1)
+    _check(lib().fp8blk_transpose_gated_weights(q_gate.data_ptr(), s_gate.data_ptr(), q_up.data_ptr(),
+                                                s_up.data_ptr(), ldq, N, K, qt.data_ptr(), ldqt,
+                                                st.data_ptr(), _stream()),
+           "fp8blk_transpose_gated_weights")
     return qt, st
 
 

@@ -188,11 +188,14 @@ RowSplit row_split(int64_t M, int64_t N) {
 // lines at a time), transposes 4 x 4 codes in registers, and the words cross
 // through shared memory: word (k, n / 4) sits in 16-byte chunk (n / 16) ^ (k / 16)
 // of row k, so that the writes (8 values of k / 16, 4 of n / 4) touch 32 different
-// banks and the reads are whole rows, 16 bytes a lane.
+// banks and the reads are whole rows, 16 bytes a lane. The second weight of a
+// gated pair (blockIdx.z = 1) goes n_end columns further right.
 __global__ void __launch_bounds__(256)
-    transpose_kernel(const uint8_t* __restrict__ q, int64_t ldq, const float* __restrict__ s,
+    transpose_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s,
+                     const uint8_t* __restrict__ q2, const float* __restrict__ s2, int64_t ldq,
                      int64_t N, int64_t K, uint8_t* __restrict__ qt, int64_t ldqt,
                      float* __restrict__ st, int64_t ldst, int64_t n_end) {
+  if (blockIdx.z) q = q2, s = s2, qt += n_end, st += gridDim.y;
   __shared__ __align__(16) uint32_t t[128 * 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t kb = blockIdx.x, nb = blockIdx.y;
@@ -252,6 +255,29 @@ __global__ void __launch_bounds__(256)
     }
   }
   if (threadIdx.x == 0) st[kb * ldst + nb] = s[nb * gridDim.x + kb];
+}
+
+// `count` weights side by side, n_end columns each.
+fp8blk_status transpose(const uint8_t* q, const float* s, const uint8_t* q2, const float* s2,
+                        int count, int64_t ldq, int64_t N, int64_t K, uint8_t* qt, int64_t ldqt,
+                        float* st, int64_t ldst, int64_t n_end, fp8blk_stream stream) {
+  if (N < 0 || K < 0) return FP8BLK_ERR_INVALID_ARG;
+  if (N == 0 || K == 0) return FP8BLK_OK;
+  if (!q || !s || !q2 || !s2 || !qt || !st || ldq < K || ldqt < count * n_end ||
+      ldst < count * cdiv(N, 128))
+    return FP8BLK_ERR_INVALID_ARG;
+  // Grid limits: blocks of K along x, of N along y.
+  if (cdiv(K, 128) > kInt32Max || cdiv(N, 128) > 65535) return FP8BLK_ERR_INVALID_ARG;
+  if (ldq % 16 || ldqt % 16 || !aligned(q, 16) || !aligned(q2, 16) || !aligned(qt, 16) ||
+      !aligned(s, 4) || !aligned(s2, 4) || !aligned(st, 4))
+    return FP8BLK_ERR_ALIGNMENT;
+  Launch L;
+  const fp8blk_status status = current_launch(stream, &L);
+  if (status != FP8BLK_OK) return status;
+  const dim3 grid(static_cast<unsigned>(cdiv(K, 128)), static_cast<unsigned>(cdiv(N, 128)),
+                  static_cast<unsigned>(count));
+  transpose_kernel<<<grid, 256, 0, L.stream>>>(q, s, q2, s2, ldq, N, K, qt, ldqt, st, ldst, n_end);
+  return cuda_status(cudaGetLastError());
 }
 
 }  // namespace
@@ -358,22 +384,17 @@ fp8blk_status fp8blk_epilogue_backward(const void* dy, int64_t lddy, const void*
 fp8blk_status fp8blk_transpose_weight(const uint8_t* q, int64_t ldq, const float* scale_inv,
                                       int64_t N, int64_t K, uint8_t* qt, int64_t ldqt, float* st,
                                       int64_t ldst, int32_t zero_pad, fp8blk_stream stream) {
-  if (N < 0 || K < 0 || (zero_pad != 0 && zero_pad != 1)) return FP8BLK_ERR_INVALID_ARG;
-  if (N == 0 || K == 0) return FP8BLK_OK;
-  const int64_t n_end = zero_pad ? round_up(N, 128) : N;
-  if (!q || !scale_inv || !qt || !st || ldq < K || ldqt < n_end || ldst < cdiv(N, 128))
-    return FP8BLK_ERR_INVALID_ARG;
-  // Grid limits: blocks of K along x, of N along y.
-  if (cdiv(K, 128) > kInt32Max || cdiv(N, 128) > 65535) return FP8BLK_ERR_INVALID_ARG;
-  if (ldq % 16 || ldqt % 16 || !aligned(q, 16) || !aligned(qt, 16) || !aligned(scale_inv, 4) ||
-      !aligned(st, 4))
-    return FP8BLK_ERR_ALIGNMENT;
-  Launch L;
-  fp8blk_status status = current_launch(stream, &L);
-  if (status != FP8BLK_OK) return status;
-  const dim3 grid(static_cast<unsigned>(cdiv(K, 128)), static_cast<unsigned>(cdiv(N, 128)));
-  transpose_kernel<<<grid, 256, 0, L.stream>>>(q, ldq, scale_inv, N, K, qt, ldqt, st, ldst, n_end);
-  return cuda_status(cudaGetLastError());
+  if (zero_pad != 0 && zero_pad != 1) return FP8BLK_ERR_INVALID_ARG;
+  return transpose(q, scale_inv, q, scale_inv, 1, ldq, N, K, qt, ldqt, st, ldst,
+                   zero_pad ? round_up(N, 128) : N, stream);
+}
+
+fp8blk_status fp8blk_transpose_gated_weights(const uint8_t* q_gate, const float* s_gate,
+                                             const uint8_t* q_up, const float* s_up, int64_t ldq,
+                                             int64_t N, int64_t K, uint8_t* qt, int64_t ldqt,
+                                             float* st, fp8blk_stream stream) {
+  return transpose(q_gate, s_gate, q_up, s_up, 2, ldq, N, K, qt, ldqt, st, 2 * cdiv(N, 128),
+                   round_up(N, 128), stream);
 }
 
 }  // extern "C"

@@ -390,7 +390,7 @@ FP8BLK_EXPORT fp8blk_status fp8blk_gated_linear_w8a8(
  *          [N, Np) and [Np + N, 2 Np) are set to 0                    (output)
  * All leading dimensions % 8 == 0. That layout is the activation operand of
  * the linears against the two transposed weights side by side (see
- * fp8blk_transpose_weight): dx = dg . Wg + du . Wu in one product. Must not
+ * fp8blk_transpose_gated_weights): dx = dg . Wg + du . Wu in one product. Must not
  * overlap. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
  * ------------------------------------------------------------------------- */
 FP8BLK_EXPORT fp8blk_status fp8blk_gated_backward(const void* dh, int64_t lddh, const void* g,
@@ -431,9 +431,6 @@ FP8BLK_EXPORT size_t fp8blk_epilogue_backward_workspace_size(int64_t M, int64_t 
  *        ldqt % 16 == 0; columns [N, round_up(N, 128)) are set to 0 if
  *        zero_pad, else not written                                   (output)
  *   st : float [ceil(K/128)][ldst], ldst >= ceil(N/128)               (output)
- * Two weights go side by side for a gated block: gate into columns [0, N) and
- * up into [Np, Np + N) of one qt with ldqt = 2 Np (Np = round_up(N, 128)),
- * both with zero_pad, and their scales into one st with ldst = 2 Np / 128.
  * Must not overlap. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
  * ------------------------------------------------------------------------- */
 FP8BLK_EXPORT fp8blk_status fp8blk_transpose_weight(const uint8_t* q, int64_t ldq,
@@ -441,6 +438,19 @@ FP8BLK_EXPORT fp8blk_status fp8blk_transpose_weight(const uint8_t* q, int64_t ld
                                                     uint8_t* qt, int64_t ldqt, float* st,
                                                     int64_t ldst, int32_t zero_pad,
                                                     fp8blk_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Both weights of a gated linear transposed side by side, the layout that
+ * fp8blk_gated_backward's output multiplies (Np = round_up(N, 128)): the gate
+ * weight in columns [0, N), the up weight in [Np, Np + N), zero codes between.
+ *   q_gate, q_up : uint8 [N][ldq]; s_gate, s_up : as above            (input)
+ *   qt : uint8 [K][ldqt], ldqt >= 2 Np, ldqt % 16 == 0                (output)
+ *   st : float [ceil(K/128)][2 Np / 128], dense                       (output)
+ * Must not overlap. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
+ * ------------------------------------------------------------------------- */
+FP8BLK_EXPORT fp8blk_status fp8blk_transpose_gated_weights(
+    const uint8_t* q_gate, const float* s_gate, const uint8_t* q_up, const float* s_up, int64_t ldq,
+    int64_t N, int64_t K, uint8_t* qt, int64_t ldqt, float* st, fp8blk_stream stream);
 
 /* ---------------------------------------------------------------------------
  * Weight gradient of a linear: dw[n][k] = sum_m dz[m][n] * x[m][k], BF16

@@ -115,6 +115,17 @@ def test_transpose_weight_validation(lib):
     assert call(N=0) == 0 and call(K=0) == 0
 
 
+def test_transpose_gated_weights_validation(lib):
+    N, K = 200, 300
+    names = "qg sg qu su ldq N K qt ldqt stt st".split()
+    call = caller(lib.fp8blk_transpose_gated_weights, names, (P, P, P, P, 304, N, K, P, 512, P, None))
+    assert call(N=-1) == 1 and call(K=-1) == 1
+    for n in ("qg", "sg", "qu", "su", "qt", "stt"):
+        assert call(**{n: None}) == 1 and call(**{n: P + 1}) == 2
+    assert call(ldq=288) == 1 and call(ldq=312) == 2 and call(ldqt=496) == 1 and call(ldqt=520) == 2
+    assert call(N=0) == 0 and call(K=0) == 0
+
+
 def test_linear_grad_weight_validation(lib):
     M, N, K = 64, 200, 304
     names = "dz lddz x ldx dw lddw fp32 add M N K ws wsb st".split()
