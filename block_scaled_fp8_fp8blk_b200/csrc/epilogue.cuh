@@ -62,6 +62,13 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return r;
 }
 
+// The larger of two; NaN if either is (fmaxf would drop it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Phi(z) = 1 - Phi(-z), and for x = |z| / sqrt 2 the tail Phi(-|z|) = erfc(x) / 2
 // = erfcx(x) exp(-x^2) / 2, which keeps its relative accuracy where 1 + erf
 // would cancel. erfcx(x) is a polynomial in t = 1 / (1 + 0.6 x), fitted to it for
@@ -97,7 +104,7 @@ __device__ __forceinline__ float act_value(const ActParams& a, float z) {
     float gauss;
     return z * act_normal(z, gauss);
   }
-  return fmaxf(z, a.lo);
+  return max_nan(z, a.lo);
 }
 
 // act of a group of values, with one branch.
@@ -114,14 +121,15 @@ __device__ __forceinline__ void act_apply(const ActParams& a, float (&v)[N]) {
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = fmaxf(v[i], a.lo);
+    for (int i = 0; i < N; ++i) v[i] = max_nan(v[i], a.lo);
   }
 }
 
-// act(z) and its derivative; relu's is 0 at 0.
+// act(z) and its derivative; relu's is 0 at 0. A NaN stays one in both (relu's
+// derivative of it is 1).
 __device__ __forceinline__ float act_slope(const ActParams& a, float z, float& value) {
   if (a.kind == kActLogistic) {
-    const float zc = fminf(fmaxf(z, -100.0f), 100.0f);
+    const float zc = -max_nan(-max_nan(z, -100.0f), -100.0f);
     const float s = act_logistic(a, zc);
     value = z * s;
     return fmaf(zc * s * (1.0f - s), (-1.0f / kLog2e) * fmaf(3.0f * a.c3, zc * zc, a.c1), s);
@@ -132,8 +140,8 @@ __device__ __forceinline__ float act_slope(const ActParams& a, float z, float& v
     value = z * cdf;
     return fmaf(z * 0.39894228040143268f, gauss, cdf);
   }
-  value = fmaxf(z, a.lo);
-  return z > a.lo ? 1.0f : 0.0f;
+  value = max_nan(z, a.lo);
+  return a.lo == 0.0f && z <= 0.0f ? 0.0f : 1.0f;
 }
 
 // What a GEMM does with its FP32 sums.

@@ -635,6 +635,40 @@ def test_repeated_calls_are_bit_identical(mode, M):
             assert same_bits(f(), first)
 
 
+@pytest.mark.parametrize("mode", ["w8a16", "w8a8"])
+@pytest.mark.parametrize("name", ACTS)
+def test_a_bad_weight_scale_shows(mode, name):
+    """A scale of NaN is outside the contract, but it must not turn into numbers:
+    its block's outputs are NaN and no others."""
+    g = gen(40)
+    M, K, N = 20, 384, 300
+    x, (q, s), wu = normal(g, M, K), weight(g, N, K), weight(g, N, K)
+    s[1, 2] = float("nan")
+    y = FUNCS["linear", mode](x, q, s, activation=name)
+    h = FUNCS["gated", mode](x, q, s, *wu, activation=name)
+    for t in (y, h):
+        assert torch.isnan(t[:, 128:256]).all()
+        assert torch.isfinite(t[:, :128]).all() and torch.isfinite(t[:, 256:]).all()
+
+
+@pytest.mark.parametrize("name", ACTS)
+def test_a_nan_stays_one_backward(name):
+    """A kept value of NaN reaches its own gradients and no others."""
+    g = gen(41)
+    M, N = 5, 140
+    dh, z, u = normal(g, M, N), normal(g, M, N), normal(g, M, N)
+    z[2, 7] = float("nan")
+    here = torch.zeros((M, N), dtype=torch.bool, device=DEV)
+    here[2, 7] = True
+    out = fb.gated_backward(dh, z, u, activation=name)
+    at = lambda t: torch.equal(torch.isnan(t), here)
+    assert at(out[:, 256:256 + N]), "du"
+    if name in ("gelu", "gelu_tanh", "silu"):
+        assert at(out[:, :N]) and at(fb.epilogue_backward(dh, z, activation=name, bias_grad=False)[0])
+    else:       # slopes of 0 and 1
+        assert torch.equal(out[2, 7].float(), (dh[2, 7].float() * u[2, 7].float()).to(torch.bfloat16).float())
+
+
 def test_refusals_of_the_binding():
     g = gen(30)
     x, (q, s) = normal(g, 4, 256), weight(g, 200, 256)
