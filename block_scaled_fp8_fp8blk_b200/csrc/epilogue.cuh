@@ -9,8 +9,10 @@
 // five names, chosen by a branch that is uniform over the grid. All of it is
 // computed in FP32 from the FP32 product; 2^x and 1/x are the approximate
 // instructions, whose error (a few units of 2^-23, growing with the exponent's
-// magnitude) is far below half a BF16 step; their subnormal results and
-// arguments count as 0.
+// magnitude) is far below half a BF16 step. Their subnormal results count as 0,
+// which would lose the far tails (silu is still a normal number at z = -92, where
+// its logistic is not), so the exponents are shifted by kTailBits and the result is
+// scaled back by a multiplication, which underflows gradually.
 //
 // What bounds this code inside a GEMM is instruction fetch: a thread holds 64
 // to 128 sums in registers, so the code is unrolled that many times and run
@@ -37,6 +39,7 @@ struct ActParams {
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTailBits = 24.0f, kTailScale = 5.9604644775390625e-8f;  // 2^-24
 
 inline bool valid_activation(int a) { return a >= FP8BLK_ACT_NONE && a <= FP8BLK_ACT_SILU; }
 
@@ -72,12 +75,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // Phi(z) = 1 - Phi(-z), and for x = |z| / sqrt 2 the tail Phi(-|z|) = erfc(x) / 2
 // = erfcx(x) exp(-x^2) / 2, which keeps its relative accuracy where 1 + erf
 // would cancel. erfcx(x) is a polynomial in t = 1 / (1 + 0.6 x), fitted to it for
-// 0 <= x <= 10 with equal relative error (3.1e-7; 6e-7 in FP32); beyond, exp(-x^2)
-// is 0 in FP32. gauss is exp(-z^2/2).
+// 0 <= x <= 10 with equal relative error (3.1e-7; 6e-7 in FP32); beyond 10.2,
+// exp(-x^2) is 0 in FP32. gauss is exp(-z^2/2).
 __device__ __forceinline__ float act_normal(float z, float& gauss) {
   const float x = fabsf(z) * 0.70710678118654752f;
   const float t = fast_rcp(fmaf(0.6f, x, 1.0f));
-  gauss = fast_exp2(-kLog2e * x * x);
+  gauss = kTailScale * fast_exp2(fmaf(-kLog2e * x, x, kTailBits));
   // (half the fitted coefficients)
   float p = 0.5f * -0.09208156913518906f;
   p = fmaf(p, t, 0.5f * 0.4119424819946289f);
@@ -91,15 +94,17 @@ __device__ __forceinline__ float act_normal(float z, float& gauss) {
   return z < 0.0f ? tail : 1.0f - tail;
 }
 
-// The logistic, 1 / (1 + 2^(c1 z + c3 z^3)). Beyond |z| = 100 it is exactly 0 or 1
-// in FP32 (the power overflows to infinity), so z is clamped there and z^3 stays
-// finite.
+// The logistic, 1 / (1 + 2^(c1 z + c3 z^3)), both terms of the sum times 2^-24.
+// At |z| = kLogisticMax it is exactly 0 or 1 in FP32 (the power is infinite or 0), so
+// z is clamped there and z^3 stays finite; from z = -104 on it is 0, and z times it
+// would be less than a thousandth of the least BF16 number.
+constexpr float kLogisticMax = 110.0f;
 __device__ __forceinline__ float act_logistic(const ActParams& a, float zc) {
-  return fast_rcp(1.0f + fast_exp2(zc * fmaf(a.c3, zc * zc, a.c1)));
+  return kTailScale * fast_rcp(kTailScale + fast_exp2(fmaf(zc, fmaf(a.c3, zc * zc, a.c1), -kTailBits)));
 }
 
 __device__ __forceinline__ float act_value(const ActParams& a, float z) {
-  if (a.kind == kActLogistic) return z * act_logistic(a, fminf(fmaxf(z, -100.0f), 100.0f));
+  if (a.kind == kActLogistic) return z * act_logistic(a, fminf(fmaxf(z, -kLogisticMax), kLogisticMax));
   if (a.kind == kActNormal) {
     float gauss;
     return z * act_normal(z, gauss);
@@ -112,7 +117,7 @@ template <int N>
 __device__ __forceinline__ void act_apply(const ActParams& a, float (&v)[N]) {
   if (a.kind == kActLogistic) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] *= act_logistic(a, fminf(fmaxf(v[i], -100.0f), 100.0f));
+    for (int i = 0; i < N; ++i) v[i] *= act_logistic(a, fminf(fmaxf(v[i], -kLogisticMax), kLogisticMax));
   } else if (a.kind == kActNormal) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -129,7 +134,7 @@ __device__ __forceinline__ void act_apply(const ActParams& a, float (&v)[N]) {
 // derivative of it is 1).
 __device__ __forceinline__ float act_slope(const ActParams& a, float z, float& value) {
   if (a.kind == kActLogistic) {
-    const float zc = -max_nan(-max_nan(z, -100.0f), -100.0f);
+    const float zc = -max_nan(-max_nan(z, -kLogisticMax), -kLogisticMax);
     const float s = act_logistic(a, zc);
     value = z * s;
     return fmaf(zc * s * (1.0f - s), (-1.0f / kLog2e) * fmaf(3.0f * a.c3, zc * zc, a.c1), s);
