@@ -39,7 +39,9 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 
 // dg = dh u act'(g), du = dh act(g): eight columns per thread, rows in steps
 // of the grid. The columns between N and Np = round_up(N, 128) get zeros (the
-// loads give dh = 0 there).
+// loads give dh = 0 there). The slope, at most 1.13 in magnitude, comes into the
+// product first: dh u alone may overflow where dg does not (and infinity times a
+// slope of 0 would be NaN).
 __global__ void __launch_bounds__(256)
     gated_backward_kernel(const uint16_t* __restrict__ dh, int64_t lddh,
                           const uint16_t* __restrict__ g, const uint16_t* __restrict__ u,
@@ -56,7 +58,7 @@ __global__ void __launch_bounds__(256)
     for (int i = 0; i < 8; ++i) {
       float a;
       const float s = act_slope(act, gv[i], a);
-      gv[i] = d[i] * uv[i] * s;
+      gv[i] = d[i] * s * uv[i];
       uv[i] = d[i] * a;
     }
     uint16_t* out = dgu + m * lddgu + c;

@@ -92,3 +92,22 @@ def test_forward_over_every_number(mode, M, name):
     value, _ = terms(name, z[0])
     for row in (y[0], y[M - 1]):
         check(row, (value,), name)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_gated_backward_products_beyond_fp32(name):
+    """dh u is beyond FP32, dg is not: the slope is 0 (the exact one of relu, or
+    below 1e-300) or, at the last z, so small that dg is an ordinary number."""
+    z = [-1e4, -200.0, -60.0, -25.0]
+    g = torch.tensor([z + z], device=DEV).to(torch.bfloat16)
+    big = torch.full_like(g, 1e20)
+    out = fb.gated_backward(big, g, big, activation=name)
+    a, slope = terms(name, g[0])
+    want = big[0].double() ** 2 * sum(slope)
+    near = want.abs() < 1e38
+    assert near[0] and near[1]
+    tol = 2.0 ** -8 * want.abs() + 2.0 ** -14 * big[0].double() ** 2 * sum(p.abs() for p in slope) + 2.0 ** -134
+    tol = tol + 2.0 ** -140 * big[0].double() ** 2      # the slope's own underflow, multiplied
+    assert bool(((out[0, :8].double() - want).abs() <= tol)[near].all()), (out[0, :8], want)
+    du = big[0].double() * a
+    assert bool(((out[0, 128:136].double() - du).abs() <= 2.0 ** -7 * du.abs() + 2.0 ** -114).all())
