@@ -57,6 +57,7 @@
 #include "epilogue.cuh"
 #include "internal.cuh"
 #include "ptx.cuh"
+#include "schedule.cuh"
 
 namespace fp8blk {
 namespace {
@@ -139,58 +140,6 @@ __device__ __forceinline__ void expand16(const uint4& c, uint32_t* o) {
 __device__ __forceinline__ uint32_t ring_parity(int item, int depth) {
   return static_cast<uint32_t>((item / depth) & 1);
 }
-
-// The slabs one CTA runs, as a run of segments (tile, [kb0, kb1)). Tiles
-// [0, dp_tiles) run whole, round robin (CTA c takes c, c + G, ...; G =
-// gridDim.x); the U = (tiles - dp_tiles) x KB slabs of the other tiles, in
-// tile-major order, run stream-K: CTA c takes the contiguous range
-// [c U / S, (c + 1) U / S) with S = min(G, U), so every CTA gets the same share
-// within one slab, and with fewer slabs than CTAs the first U take one each
-// (a CTA in the middle of a split tile must not be without a slab: the
-// fix-up reads a partial from every CTA between the tile's first and last).
-// A stream-K tile may be split across consecutive CTAs; only a CTA's first
-// and last stream-K segments can be partial. dp_tiles = 0 is pure stream-K,
-// dp_tiles = tiles pure round robin.
-// (Slab counts fit in 32 bits: the host checks tiles x KB.)
-// FEW: U may be smaller than G (with one sub-tile the host launches at most U CTAs).
-template <bool FEW>
-struct Schedule {
-  int u, end, first;
-  int tile, KB, dp_tiles;
-  __device__ Schedule(int kb_per_tile, int tiles, int dp)
-      : tile(static_cast<int>(blockIdx.x)), KB(kb_per_tile), dp_tiles(dp) {
-    const int64_t U = static_cast<int64_t>(tiles - dp) * kb_per_tile;
-    if constexpr (FEW) {
-      const int64_t S = U < gridDim.x ? U : gridDim.x;
-      const bool some = blockIdx.x < S;
-      first = u = some ? static_cast<int>(U * blockIdx.x / S) : 0;
-      end = some ? static_cast<int>(U * (blockIdx.x + 1) / S) : 0;
-    } else {
-      first = u = static_cast<int>(U * blockIdx.x / gridDim.x);
-      end = static_cast<int>(U * (blockIdx.x + 1) / gridDim.x);
-    }
-  }
-  __device__ int slabs() const {
-    const int dp = tile < dp_tiles ? ((dp_tiles - 1 - tile) / static_cast<int>(gridDim.x) + 1) * KB : 0;
-    return dp + (end - first);
-  }
-  __device__ bool next(int& t, int& kb0, int& kb1) {
-    if (tile < dp_tiles) {
-      t = tile;
-      kb0 = 0;
-      kb1 = KB;
-      tile += static_cast<int>(gridDim.x);
-      return true;
-    }
-    if (u >= end) return false;
-    const int lt = u / KB;
-    t = dp_tiles + lt;
-    kb0 = u - lt * KB;
-    kb1 = min(KB, kb0 + (end - u));
-    u += kb1 - kb0;
-    return true;
-  }
-};
 
 // ------------------------------------------------------------------ expansion
 // One warpgroup expands the slabs j = eg, eg + NEXP, ... of its CTA: thread r
@@ -456,7 +405,7 @@ __global__ void __launch_bounds__(512, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   using Sched = Schedule<NSUB == 2>;
-  const int total_slabs = Sched(KB, ntiles_total, dp_tiles).slabs();
+  const int total_slabs = Sched(KB, ntiles_total, dp_tiles, blockIdx.x, gridDim.x).slabs();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::QS; ++s) {
@@ -505,7 +454,7 @@ __global__ void __launch_bounds__(512, 1)
       if (!early_weights) pdl_wait();
       int j = 0;  // slab counter (across tiles)
       bool ok = true;
-      Sched sc(KB, ntiles_total, dp_tiles);
+      Sched sc(KB, ntiles_total, dp_tiles, blockIdx.x, gridDim.x);
       int tile, kb0, kb1;
       while (ok && sc.next(tile, kb0, kb1)) {
         int mt, nt;
@@ -530,7 +479,7 @@ __global__ void __launch_bounds__(512, 1)
       pdl_wait();
       int i = 0;  // item counter (across tiles)
       bool ok = true;
-      Sched sc(KB, ntiles_total, dp_tiles);
+      Sched sc(KB, ntiles_total, dp_tiles, blockIdx.x, gridDim.x);
       int tile, kb0, kb1;
       while (ok && sc.next(tile, kb0, kb1)) {
         int mt, nt;
@@ -618,7 +567,7 @@ __global__ void __launch_bounds__(512, 1)
       int j = 0;
       bool ok = true;
       bool first_sk = true;  // the next stream-K segment is this CTA's first
-      Sched sc(KB, ntiles_total, dp_tiles);
+      Sched sc(KB, ntiles_total, dp_tiles, blockIdx.x, gridDim.x);
       int tile, kb0, kb1;
       while (ok && sc.next(tile, kb0, kb1)) {
         int mt, nt;
@@ -716,7 +665,7 @@ __global__ void __launch_bounds__(512, 1)
       const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16) + C::TMEM_P;
       int j = 0;
       bool ok = true;
-      Sched sc(KB, ntiles_total, dp_tiles);
+      Sched sc(KB, ntiles_total, dp_tiles, blockIdx.x, gridDim.x);
       int tile, kb0, kb1;
       bool first_segment = true;
       while (ok && sc.next(tile, kb0, kb1)) {
@@ -817,42 +766,6 @@ __global__ void __launch_bounds__(512, 1)
   }
 }
 
-// CTAs a stream-K launch may use (the workspace is sized for this many).
-constexpr int kStreamKMaxCtas = 160;
-
-// The tiles a stream-K launch splits across CTAs, worked out on the host:
-// CTA c holds slabs [c U / G, (c + 1) U / G) of the U = tiles x KB slabs (G the
-// CTAs that have any: at most U), so
-// a tile is split when a range boundary falls inside it. Each split tile
-// lists its first contributor c0 (whose last segment it is), the number of
-// contributors, and the workspace slot c0 wrote (0 if the tile was also
-// c0's first segment, else 1); later contributors wrote slot 0.
-struct SplitTiles {
-  int count;
-  int tile[kStreamKMaxCtas];
-  short c0[kStreamKMaxCtas];
-  unsigned char ncontrib[kStreamKMaxCtas];
-  unsigned char slot0[kStreamKMaxCtas];
-};
-
-SplitTiles split_tiles(int64_t ntiles, int64_t KB, int64_t G) {
-  SplitTiles st{};
-  const int64_t U = ntiles * KB;
-  for (int64_t c0 = 0; c0 + 1 < G; ++c0) {
-    const int64_t x = U * (c0 + 1) / G;  // first slab of CTA c0 + 1
-    const int64_t t = x / KB, s0 = t * KB;
-    const int64_t c0_start = U * c0 / G;
-    if (x == s0 || c0_start > s0) continue;  // no split here, or not the tile's first boundary
-    const int64_t c1 = ((s0 + KB) * G - 1) / U;  // holds the tile's last slab
-    st.tile[st.count] = static_cast<int>(t);
-    st.c0[st.count] = static_cast<short>(c0);
-    st.ncontrib[st.count] = static_cast<unsigned char>(c1 - c0 + 1);
-    st.slot0[st.count] = static_cast<unsigned char>(c0_start == s0 ? 0 : 1);
-    ++st.count;
-  }
-  return st;
-}
-
 // Stream-K fix-up: y of every split tile, the sum of its contributors' FP32
 // partials in slab order, rounded once to BF16. Block (i, g) handles split
 // tile i for tokens [8 g, 8 g + 8) of its TOK with one thread per weight row
@@ -930,19 +843,6 @@ __global__ void __launch_bounds__(256) w8a16_streamk_fixup(const __grid_constant
   }
 }
 
-// Workspace bytes of a stream-K launch with grid CTAs and TOK-token tiles:
-// two FP32 partial slots of [TOK][128] per CTA.
-size_t streamk_bytes(int64_t grid, int tok) {
-  return static_cast<size_t>(grid) * 2 * tok * 128 * sizeof(float);
-}
-
-// What the stream-K fix-up costs a call, in slabs of one CTA's time (a slab takes
-// about twice as long with 128 tokens). Measured, split -> whole, one token: 512
-// inputs and 5120 outputs (4 slabs in sequence against 2) 16.4 -> 12.3 us, 1024 and 10240
-// (8 against 5) 18.4 -> 14.4, 2048 and 256 (16 against 1) 14.3 -> 16.4; 128 tokens: 512 and
-// 5120 20.5 -> 16.4, 1024 and 256 (8 against 1) 16.4 -> 18.4.
-constexpr int64_t fixup_slabs(int bt) { return bt >= 128 ? 5 : 11; }
-
 template <int BT, int NSUB, bool GROUPED, int EPI>
 cudaError_t launch_bt(const Launch& L, const uint16_t* x, int64_t ldx, const uint8_t* q,
                       int64_t ldq, const float* sw, uint16_t* y, int64_t ldy, int64_t M,
@@ -980,39 +880,15 @@ cudaError_t launch_bt(const Launch& L, const uint16_t* x, int64_t ldx, const uin
   // Slab and item counters are 32-bit per CTA.
   if (tiles * cdiv(K, 128) * NSUB > 0x7FFFFFFFLL) return cudaErrorInvalidValue;
   const int64_t KB = cdiv(K, 128);
-  const int64_t G = L.num_sms < kStreamKMaxCtas ? L.num_sms : kStreamKMaxCtas;
-  int64_t dp_tiles, grid;
+  SlabPlan plan;
   if (NSUB == 1) {
-    // One token tile (M <= 128): stream-K over all the slabs, so every SM
-    // streams the same share of the weights however few tiles there are.
-    dp_tiles = 0;
-    grid = tiles * KB < G ? tiles * KB : G;
-    if (EPI != kEpiPlain && cdiv(tiles, G) * KB <= cdiv(tiles * KB, G) + fixup_slabs(BT)) {
-      // Whole tiles where the even split would save less than its fix-up costs.
-      // (The plain linear keeps its order of sums.)
-      dp_tiles = tiles;
-      grid = tiles < G ? tiles : G;
-    }
-    if (!ws || ws_bytes < streamk_bytes(grid, TOK)) return cudaErrorInvalidValue;
+    plan = one_token_tile_plan(tiles, KB, L.num_sms, BT, EPI != kEpiPlain);
+    if (!ws || ws_bytes < streamk_bytes(plan.grid, TOK)) return cudaErrorInvalidValue;
   } else {
-    // Whole tiles round robin. When the last wave of tiles would leave at
-    // least 15% of the SM time idle, and the workspace allows, the tiles of
-    // that wave run stream-K over all CTAs instead. (Below that the partial
-    // round trip and the fix-up cost what the even split saves: at 10% idle
-    // -- 400 tiles on 148 SMs -- both ran in the same time.)
-    const int64_t waves = tiles / G, rem = tiles - waves * G;
-    const int64_t tail_grid = waves > 0 ? G : (rem * KB < G ? rem * KB : G);
-    const bool tail_sk = rem > 0 && (G - rem) * 100 >= 15 * (waves + 1) * G && tail_grid >= 2 && ws &&
-                         reinterpret_cast<uintptr_t>(ws) % 256 == 0 &&
-                         ws_bytes >= streamk_bytes(tail_grid, TOK);
-    if (tail_sk) {
-      dp_tiles = waves * G;
-      grid = tail_grid;
-    } else {
-      dp_tiles = tiles;
-      grid = tiles < L.num_sms ? tiles : L.num_sms;
-    }
+    const bool usable = ws && reinterpret_cast<uintptr_t>(ws) % 256 == 0;
+    plan = many_token_tiles_plan(tiles, KB, L.num_sms, usable ? ws_bytes : 0);
   }
+  const int64_t dp_tiles = plan.dp_tiles, grid = plan.grid;
   // A programmatic dependent of the kernel before it in the stream (its set-up
   // overlaps that kernel's tail; see the kernel for what waits).
   {
@@ -1053,8 +929,6 @@ cudaError_t launch_bt(const Launch& L, const uint16_t* x, int64_t ldx, const uin
                             ldy, static_cast<int>(M), static_cast<int>(N), static_cast<int>(mtiles),
                             gm, ep);
 }
-
-int token_tile(int64_t M) { return M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128)); }
 
 template <int EPI>
 cudaError_t launch_epi(const Launch& L, const uint16_t* x, int64_t ldx, const uint8_t* q,

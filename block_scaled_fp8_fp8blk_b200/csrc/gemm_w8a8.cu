@@ -66,6 +66,7 @@
 #include "epilogue.cuh"
 #include "internal.cuh"
 #include "ptx.cuh"
+#include "schedule.cuh"
 
 namespace fp8blk {
 namespace {
@@ -734,36 +735,16 @@ int64_t resident_clusters() {
   return n;
 }
 
-// CTAs per tile: the least of rounds x (slabs per CTA + what a round costs
-// besides), in slabs (0.5 us each here): a start and an end of about kRoundSlabs,
-// and for the trade kTradeSlabs, more with two CTAs, where each finishes half of
-// a tile. At least kMinSplitSlabs slabs each. Measured (one CTA per tile -> this rule,
-// 16 tokens, residual): 25600 -> 5120 121 -> 47 us, 8192 -> 5120
-// 49 -> 25, 4096 -> 2560 33 -> 16, 8192 -> 16384 51 -> 45, 1024 -> 5120 18 -> 16.
-constexpr int64_t kRoundSlabs = 8, kTradeSlabs = 4, kTradeSlabs2 = 16, kMinSplitSlabs = 2;
-template <int EPI>
-int split_of(int64_t tiles, int64_t KB, int num_sms) {
-  int best = 1;
-  int64_t cost = cdiv(tiles, num_sms) * (KB + kRoundSlabs);
-  if (tiles * 2 > num_sms || KB < 2 * kMinSplitSlabs) return 1;  // not few, or nothing to share
-  auto consider = [&](int s, int64_t resident, int64_t trade) {
-    if (resident <= 0 || KB < s * kMinSplitSlabs) return;
-    const int64_t c = cdiv(tiles, resident) * (cdiv(KB, s) + kRoundSlabs + trade);
-    if (c < cost) cost = c, best = s;
-  };
-  consider(2, resident_clusters<EPI, 2>(), kTradeSlabs2);
-  consider(4, resident_clusters<EPI, 4>(), kTradeSlabs);
-  consider(8, resident_clusters<EPI, 8>(), kTradeSlabs);
-  return best;
-}
-
 template <int EPI>
 cudaError_t launch_split(const Launch& L, const uint8_t* qx, int64_t ldqx, const float* sx,
                          int64_t ldsx, const uint8_t* q, int64_t ldq, const float* sw, uint16_t* y,
                          int64_t ldy, int64_t M, int64_t N, int64_t K, EpiParams<EPI>& ep) {
   using C = W8A8Cfg;
   const int64_t tiles = cdiv(M, C::BM) * cdiv(N, EPI == kEpiGated ? C::BN / 2 : C::BN);
-  switch (split_of<EPI>(tiles, cdiv(K, 128), L.num_sms)) {
+  const int split = ctas_per_tile(tiles, cdiv(K, 128), L.num_sms, [](int s) {
+    return s == 2 ? resident_clusters<EPI, 2>() : s == 4 ? resident_clusters<EPI, 4>() : resident_clusters<EPI, 8>();
+  });
+  switch (split) {
     case 8: return launch_epi<EPI, 8>(L, qx, ldqx, sx, ldsx, q, ldq, sw, y, ldy, M, N, K, true, ep);
     case 4: return launch_epi<EPI, 4>(L, qx, ldqx, sx, ldsx, q, ldq, sw, y, ldy, M, N, K, true, ep);
     case 2: return launch_epi<EPI, 2>(L, qx, ldqx, sx, ldsx, q, ldq, sw, y, ldy, M, N, K, true, ep);
