@@ -546,22 +546,26 @@ def epilogue_backward(dy, z=None, activation="none", dz=None, bias_grad=True, wo
     return dz, dbias
 
 
-def transpose_weight(q, scale_inv, qt=None, st=None):
+def transpose_weight(q, scale_inv, qt=None, st=None, zero_pad=False):
     """(qt, st): the transposed block-FP8 weight, codes [K, N] and scales
-    [ceil(K/128), ceil(N/128)], exact. dx = linear_w8a16(dz, qt, st)."""
+    [ceil(K/128), ceil(N/128)], exact. dx = linear_w8a16(dz, qt, st).
+
+    zero_pad: codes [K, Np] with Np = round_up(N, 128), zeros in the columns past
+    N, for a dz in a buffer of Np columns whose last ones hold any numbers."""
     import torch
     N, K = _dims(q, "q")
     dev = _device(q, "q")
     ldq = _weight(q, scale_inv, N, K, dev, "weight")
+    cols = _round_up(N, 128) if zero_pad else N
     if st is None:
         st = torch.empty((_cdiv(K, 128), _cdiv(N, 128)), dtype=torch.float32, device=dev)
     if qt is None:
-        qt, ldqt = _new(K, N, 16, torch.uint8, dev)
+        qt, ldqt = _new(K, cols, 16, torch.uint8, dev)
         _scales(st, K, N, dev, "transposed weight")
     else:
-        ldqt = _weight(qt, st, K, N, dev, "transposed weight")
+        ldqt = _weight(qt, st, K, cols, dev, "transposed weight")
     _check(lib().fp8blk_transpose_weight(q.data_ptr(), ldq, scale_inv.data_ptr(), N, K, qt.data_ptr(),
-                                         ldqt, st.data_ptr(), st.shape[1], 0, _stream()),
+                                         ldqt, st.data_ptr(), st.shape[1], int(bool(zero_pad)), _stream()),
            "fp8blk_transpose_weight")
     return qt, st
 
