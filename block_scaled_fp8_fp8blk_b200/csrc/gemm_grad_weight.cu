@@ -371,9 +371,9 @@ __global__ void __launch_bounds__(256)
 // How the tokens are split: runs of whole stages, chosen from the sizes alone (for
 // the 74 CTA pairs of a B200; the sums do not depend on how many there are). Runs
 // are at least kMinRunSteps stages (512 tokens) long, and all units run at once.
-// Measured, whole -> split with runs of at least 256 tokens, 1024 x 1024 weights:
-// 512 tokens 14.3 -> 16.4 us, 1024 16.4 -> 18.4, 2048 20.5 -> 18.4, 4096 30.7 -> 22.5;
-// 256 x 256, 4096 tokens 30.7 -> 16.4.
+// Measured, whole -> split, FP32 out: 1024 x 1024 weights, 1024 tokens 11.5 -> 12.2 us,
+// 2048 16.4 -> 14.3, 4096 26.4 -> 17.0; 256 x 256, 1024 tokens 11.0 -> 10.0, 4096 25.4 ->
+// 11.5. With runs of 256 tokens, 512 tokens of 1024 x 1024 went 8.9 -> 10.8, 1024 -> 12.6.
 constexpr int64_t kGradPairs = 74, kMinRunSteps = 8;
 struct TokenSplit {
   int64_t run_steps, runs;

@@ -108,10 +108,17 @@ inline size_t streamk_bytes(int64_t grid, int tok) {
 }
 
 // What the stream-K fix-up costs a call, in slabs of one CTA's time (a slab takes
-// about twice as long with 128 tokens). Measured, split -> whole, one token: 512
-// inputs and 5120 outputs (4 slabs in sequence against 2) 16.4 -> 12.3 us, 1024 and 10240
-// (8 against 5) 18.4 -> 14.4, 2048 and 256 (16 against 1) 14.3 -> 16.4; 128 tokens: 512 and
-// 5120 20.5 -> 16.4, 1024 and 256 (8 against 1) 16.4 -> 18.4.
+// about twice as long with 128 tokens). Measured, whole minus split in us (device time,
+// clean L2), range and median over 20, 40, 74, 110, 200 and 400 tiles of 4 to 68 slabs,
+// by the slabs that the split saves:
+//                1, 24, 64 tokens   8 saved           11                14                20
+//   with residual             -6.8 .. -1.6 (-3.6)  -4.1 .. 0.1 (-1.9)  -3.2 .. 1.6 (-0.7)  -2.7 .. 3.9 (1.2)
+//   gated                     -3.7 .. -0.1 (-1.8)  -1.3 .. 1.3 (-0.4)  -0.6 .. 2.8 (1.2)    0.6 .. 5.1 (2.8)
+//                128 tokens         3 saved           5                 7                 10
+//   with residual             -5.7 .. -0.6 (-4.7)  -4.6 .. -0.5 (-3.4)  -3.0 .. 0.8 (-2.4)  -2.1 .. 3.8 (-0.3)
+//   gated                     -2.9 .. 0.8 (-1.7)   -1.7 .. 1.2 (-1.0)  -0.4 .. 2.4 (0.6)    0.3 .. 9.5 (2.4)
+// The medians cross near 12 and 6 with the gate and near 15 and 10 with a residual; one
+// number for both forms, just below the lower of the two.
 constexpr int64_t fixup_slabs(int token_tile) { return token_tile >= 128 ? 5 : 11; }
 
 // The launch of a W8A16 GEMM: the first dp_tiles tiles whole, the others split.
@@ -150,8 +157,9 @@ inline SlabPlan many_token_tiles_plan(int64_t tiles, int64_t KB, int num_sms, si
 // CTA + what a round costs besides), in slabs (0.5 us each here): a start and an end
 // of about kRoundSlabs, and for the trade kTradeSlabs, more with two CTAs, where each
 // finishes half of a tile. At least kMinSplitSlabs slabs each. Measured (one CTA per
-// tile -> this rule, 16 tokens, residual): 25600 -> 5120 121 -> 47 us, 8192 -> 5120
-// 49 -> 25, 4096 -> 2560 33 -> 16, 8192 -> 16384 51 -> 45, 1024 -> 5120 18 -> 16.
+// tile -> this rule, 16 tokens, residual): 25600 -> 5120 119 -> 48 us, 8192 -> 5120
+// 44 -> 23, 4096 -> 2560 25 -> 13, 1024 -> 5120 12.5 -> 12.3; two CTAs: 8192 -> 16384
+// 50 -> 43, 5120 -> 16384 35 -> 32, and at the border 4224 -> 16384 30.1 -> 29.8.
 // resident(s): clusters of s CTAs that can be resident at once (0: none).
 constexpr int64_t kRoundSlabs = 8, kTradeSlabs = 4, kTradeSlabs2 = 16, kMinSplitSlabs = 2;
 template <class F>
