@@ -600,8 +600,8 @@ def linear_grad_weight_workspace_size(M: int, N: int, K: int) -> int:
 
 def linear_grad_weight(dz, x, out=None, accumulate=False, dtype=None, workspace=None):
     """dw [N, K] = dz^T . x over the tokens of dz BF16 [M, N] and x BF16 [M, K],
-    FP32 sums; float32 unless out or dtype says BF16. accumulate adds to a
-    float32 out."""
+    FP32 sums of the products of the BF16 values given; float32 unless out or
+    dtype says BF16. accumulate adds to a float32 out."""
     import torch
     bf16, f32 = torch.bfloat16, torch.float32
     M, N = _dims(dz, "dz")

@@ -5,6 +5,13 @@
 // Each touches every byte once: 16-byte loads and stores along the rows,
 // enough of them in flight per SM to cover the latency of HBM, and nothing
 // kept between kernels but the column sums of the bias gradient.
+//
+// dg, du and dz leave FP32 here, rounded to BF16 once: they are the operands of the
+// tensor cores' products that follow, whose kind takes BF16 on both sides, and the
+// traffic of these kernels (FP32 copies would take half as much time again, and
+// a second BF16 term to carry the rest would double the products). What is
+// computed from them carries that rounding: a relative norm of 1.7e-3 in dx and dw
+// before their own. The bias gradient is summed before it.
 #include <cuda_runtime.h>
 
 #include "epilogue.cuh"
