@@ -280,6 +280,7 @@ fp8blk_status transpose(const uint8_t* q, const float* s, const uint8_t* q2, con
   if (ldq % 16 || ldqt % 16 || !aligned(q, 16) || !aligned(q2, 16) || !aligned(qt, 16) ||
       !aligned(s, 4) || !aligned(s2, 4) || !aligned(st, 4))
     return FP8BLK_ERR_ALIGNMENT;
+  if (one_of(qt, q, q2) || one_of(st, s, s2)) return FP8BLK_ERR_INVALID_ARG;
   Launch L;
   const fp8blk_status status = current_launch(stream, &L);
   if (status != FP8BLK_OK) return status;
@@ -307,6 +308,7 @@ fp8blk_status fp8blk_gated_backward(const void* dh, int64_t lddh, const void* g,
   if (lddh % 8 || ldgu % 8 || lddgu % 8 || !aligned(dh, 16) || !aligned(g, 16) || !aligned(u, 16) ||
       !aligned(dgu, 16))
     return FP8BLK_ERR_ALIGNMENT;
+  if (one_of(dgu, dh, g, u)) return FP8BLK_ERR_INVALID_ARG;
   Launch L;
   fp8blk_status st = current_launch(stream, &L);
   if (st != FP8BLK_OK) return st;
@@ -354,6 +356,7 @@ fp8blk_status fp8blk_epilogue_backward(const void* dy, int64_t lddy, const void*
         return FP8BLK_ERR_WORKSPACE;
     }
   }
+  if (M > 0 && one_of(dbias, dy, z, dz)) return FP8BLK_ERR_INVALID_ARG;
   if (identity && dz == dy) dz = nullptr;  // already there
   if (M > 0 && !dz && !dbias) return FP8BLK_OK;
   Launch L;

@@ -47,6 +47,9 @@ fp8blk_status linear_epilogue(int mode, const void* x, int64_t ldx, const uint8_
   if (ep->residual == y && ep->ldr != ldy) return FP8BLK_ERR_INVALID_ARG;
   if (ep->preact && (st = check_matrix(ep->preact, ep->ldp, N)) != FP8BLK_OK) return st;
   if (ep->preact && (ep->preact == y || ep->preact == ep->residual)) return FP8BLK_ERR_INVALID_ARG;
+  // An output over an input would be written while other tiles still read it.
+  for (const void* out : {static_cast<const void*>(y), static_cast<const void*>(ep->preact)})
+    if (one_of(out, ep->bias) || (K > 0 && one_of(out, x, q, scale_inv))) return FP8BLK_ERR_INVALID_ARG;
   Launch L;
   st = current_launch(stream, &L);
   if (st != FP8BLK_OK) return st;
@@ -93,6 +96,8 @@ fp8blk_status gated_linear(int mode, const void* x, int64_t ldx, const uint8_t* 
     if ((st = check_matrix(u, ldgu, N)) != FP8BLK_OK) return st;
     if (g == u || g == h || u == h) return FP8BLK_ERR_INVALID_ARG;
   }
+  for (const void* out : {h, g, u})
+    if (K > 0 && one_of(out, x, q_gate, s_gate, q_up, s_up)) return FP8BLK_ERR_INVALID_ARG;
   Launch L;
   st = current_launch(stream, &L);
   if (st != FP8BLK_OK) return st;

@@ -511,6 +511,7 @@ fp8blk_status fp8blk_linear_grad_weight(const void* dz, int64_t lddz, const void
   if (M > 0) {
     if (!dz || !x || lddz < N || ldx < K) return FP8BLK_ERR_INVALID_ARG;
     if (lddz % 8 || ldx % 8 || !aligned(dz, 16) || !aligned(x, 16)) return FP8BLK_ERR_ALIGNMENT;
+    if (one_of(dw, dz, x)) return FP8BLK_ERR_INVALID_ARG;
   } else if (accumulate) {
     return FP8BLK_OK;
   }

@@ -108,6 +108,12 @@ inline int64_t w8a8_ldsx(int64_t M) { return round_up(M, 128); }
 inline int64_t w8a8_sx_offset(int64_t M, int64_t K) { return round_up(M * w8a8_ldqx(K), 256); }
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+// Whether p (not null) is one of the pointers: an output given as an input, or the other
+// way round. (Ranges are not compared: columns of one buffer interleave.)
+template <class... P>
+bool one_of(const void* p, const P*... others) {
+  return p && ((p == static_cast<const void*>(others)) || ...);
+}
 inline fp8blk_status cuda_status(cudaError_t e) {
   return e == cudaSuccess ? FP8BLK_OK : FP8BLK_ERR_CUDA;
 }

@@ -312,9 +312,10 @@ FP8BLK_EXPORT fp8blk_status fp8blk_streamed_linears(const fp8blk_linear_job* job
  *   SILU       z / (1 + exp(-z))
  * All of them are computed in FP32 from FP32 sums; BF16 results are rounded
  * once, to nearest even. That includes dg, du and dz below, so input and weight
- * gradients made from them (an FP32 weight gradient too) are exact sums of rounded
+ * gradients made from them (an FP32 weight gradient too) are FP32 sums of rounded
  * terms: 1.7e-3 in relative norm from those of unrounded ones, the size of one BF16
- * rounding.
+ * rounding. Outputs must not overlap inputs or one another, except where a call says
+ * so; the same pointer for both is refused with INVALID_ARG.
  * ------------------------------------------------------------------------- */
 typedef enum fp8blk_activation {
   FP8BLK_ACT_NONE = 0,
@@ -370,7 +371,6 @@ FP8BLK_EXPORT fp8blk_status fp8blk_linear_w8a8_epilogue(
  *          sums); ldgu >= N, ldgu % 8 == 0                            (output)
  *   workspace : as for the linear calls, for 2 N outputs: fp8blk_workspace_size(
  *          mode, M, 2 * N, K) bytes, required and optional as there.
- * Outputs must not overlap the inputs or one another.
  * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, WORKSPACE, CUDA.
  * ------------------------------------------------------------------------- */
 FP8BLK_EXPORT fp8blk_status fp8blk_gated_linear_w8a16(
@@ -393,8 +393,8 @@ FP8BLK_EXPORT fp8blk_status fp8blk_gated_linear_w8a8(
  *          [N, Np) and [Np + N, 2 Np) are set to 0                    (output)
  * All leading dimensions % 8 == 0. That layout is the activation operand of
  * the linears against the two transposed weights side by side (see
- * fp8blk_transpose_gated_weights): dx = dg . Wg + du . Wu in one product. Must not
- * overlap. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
+ * fp8blk_transpose_gated_weights): dx = dg . Wg + du . Wu in one product.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
  * ------------------------------------------------------------------------- */
 FP8BLK_EXPORT fp8blk_status fp8blk_gated_backward(const void* dh, int64_t lddh, const void* g,
                                                   const void* u, int64_t ldgu, int32_t activation,
@@ -434,7 +434,7 @@ FP8BLK_EXPORT size_t fp8blk_epilogue_backward_workspace_size(int64_t M, int64_t 
  *        ldqt % 16 == 0; columns [N, round_up(N, 128)) are set to 0 if
  *        zero_pad, else not written                                   (output)
  *   st : float [ceil(K/128)][ldst], ldst >= ceil(N/128)               (output)
- * Must not overlap. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
  * ------------------------------------------------------------------------- */
 FP8BLK_EXPORT fp8blk_status fp8blk_transpose_weight(const uint8_t* q, int64_t ldq,
                                                     const float* scale_inv, int64_t N, int64_t K,
@@ -449,7 +449,7 @@ FP8BLK_EXPORT fp8blk_status fp8blk_transpose_weight(const uint8_t* q, int64_t ld
  *   q_gate, q_up : uint8 [N][ldq]; s_gate, s_up : as above            (input)
  *   qt : uint8 [K][ldqt], ldqt >= 2 Np, ldqt % 16 == 0                (output)
  *   st : float [ceil(K/128)][2 Np / 128], dense                       (output)
- * Must not overlap. Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED_DEVICE, CUDA.
  * ------------------------------------------------------------------------- */
 FP8BLK_EXPORT fp8blk_status fp8blk_transpose_gated_weights(
     const uint8_t* q_gate, const float* s_gate, const uint8_t* q_up, const float* s_up, int64_t ldq,
