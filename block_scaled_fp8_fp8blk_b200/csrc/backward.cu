@@ -30,13 +30,13 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&v)[8]) {
 
 // Eight BF16 values of a row from column c on: one 16-byte load where all
 // eight exist, else the existing ones and zeros.
-__device__ __forceinline__ void load8(const uint16_t* row, int64_t c, int64_t n, float (&v)[8]) {
-  if (c + 8 <= n) {
-    unpack8(*reinterpret_cast<const uint4*>(row + c), v);
-  } else {
+__device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t c, int64_t n) {
+  if (c + 8 <= n) return *reinterpret_cast<const uint4*>(row + c);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < n ? bf16_bits_to_f32(row[c + i]) : 0.0f;
-  }
+  for (int i = 0; i < 8; ++i)
+    if (c + i < n) w[i / 2] |= static_cast<uint32_t>(row[c + i]) << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
@@ -44,11 +44,34 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     cvt_bf16x2(v[7], v[6]));
 }
 
-// dg = dh u act'(g), du = dh act(g): eight columns per thread, rows in steps
-// of the grid. The columns between N and Np = round_up(N, 128) get zeros (the
-// loads give dh = 0 there). The slope, at most 1.13 in magnitude, comes into the
-// product first: dh u alone may overflow where dg does not (and infinity times a
-// slope of 0 would be NaN).
+// dg = dh u act'(g), du = dh act(g) of eight columns. The slope, at most 1.13 in
+// magnitude, comes into the product first: dh u alone may overflow where dg does
+// not (and infinity times a slope of 0 would be NaN).
+template <int KIND>
+__device__ __forceinline__ void gated_slopes(ActParams act, const uint4& d, const uint4& g,
+                                             const uint4& u, uint4& dg, uint4& du) {
+  act.kind = KIND;
+  const uint32_t dw[4] = {d.x, d.y, d.z, d.w}, gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+  uint32_t a[4], b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float v0, v1;
+    const float s0 = act_slope(act, bf16_lo_to_f32(gw[i]), v0);
+    const float s1 = act_slope(act, bf16_hi_to_f32(gw[i]), v1);
+    const float d0 = bf16_lo_to_f32(dw[i]), d1 = bf16_hi_to_f32(dw[i]);
+    a[i] = cvt_bf16x2(d1 * s1 * bf16_hi_to_f32(uw[i]), d0 * s0 * bf16_lo_to_f32(uw[i]));
+    b[i] = cvt_bf16x2(d1 * v1, d0 * v0);
+  }
+  dg = make_uint4(a[0], a[1], a[2], a[3]);
+  du = make_uint4(b[0], b[1], b[2], b[3]);
+}
+
+// Eight columns per thread, rows in steps of the grid. The columns between N and
+// Np = round_up(N, 128) get zeros (the loads give dh = 0 there). Bound by HBM, so the
+// loads in flight count: one branch on the activation per eight columns and operands
+// unpacked as they are used take 35 registers, seven blocks an SM. Unpacked in
+// advance with the branch in each element, 57 and four: 84 us against 78 at 2048 x
+// 25600 with silu (cleared L2), 166 against 160 at 4096 with gelu.
 __global__ void __launch_bounds__(256)
     gated_backward_kernel(const uint16_t* __restrict__ dh, int64_t lddh,
                           const uint16_t* __restrict__ g, const uint16_t* __restrict__ u,
@@ -57,20 +80,19 @@ __global__ void __launch_bounds__(256)
   const int64_t c = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
   if (c >= Np) return;
   for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
-    float d[8], gv[8], uv[8];
-    load8(dh + m * lddh, c, N, d);
-    load8(g + m * ldgu, c, N, gv);
-    load8(u + m * ldgu, c, N, uv);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float a;
-      const float s = act_slope(act, gv[i], a);
-      gv[i] = d[i] * s * uv[i];
-      uv[i] = d[i] * a;
+    const uint4 d = load8(dh + m * lddh, c, N), gv = load8(g + m * ldgu, c, N),
+                uv = load8(u + m * ldgu, c, N);
+    uint4 dg, du;
+    if (act.kind == kActLogistic) {
+      gated_slopes<kActLogistic>(act, d, gv, uv, dg, du);
+    } else if (act.kind == kActNormal) {
+      gated_slopes<kActNormal>(act, d, gv, uv, dg, du);
+    } else {
+      gated_slopes<kActMax>(act, d, gv, uv, dg, du);
     }
     uint16_t* out = dgu + m * lddgu + c;
-    *reinterpret_cast<uint4*>(out) = pack8(gv);
-    *reinterpret_cast<uint4*>(out + Np) = pack8(uv);
+    *reinterpret_cast<uint4*>(out) = dg;
+    *reinterpret_cast<uint4*>(out + Np) = du;
   }
 }
 
@@ -148,8 +170,8 @@ __global__ void __launch_bounds__(256, 4)
 #pragma unroll 1
     for (; m < m1; m += kRowsPerStep) {
       float d[8], v[8];
-      load8(dy + m * lddy, c, N, d);
-      if (z) load8(z + m * ldz, c, N, v);
+      unpack8(load8(dy + m * lddy, c, N), d);
+      if (z) unpack8(load8(z + m * ldz, c, N), v);
       epilogue_backward_row<SUM>(d, v, z != nullptr, act, row_out(m), c, N, sum);
     }
   }
